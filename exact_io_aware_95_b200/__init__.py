@@ -47,6 +47,16 @@ EXPORTS = {
     "fa_fwd_fp8": (_I, [_P, _P, _P, _F, _F, _F, _P, _P, _P, _S, _I, _I, _I, _I, _F, _I, _P]),
     "fa_decode_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _F, _I, _P]),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
+    "fa_mask_plan_size": (_S, [_I, _I]),
+    "fa_mask_plan": (_I, [_P, _S, _P, _P, _I, _I, _I, _I, _P]),
+    "fa_mod_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
+    "fa_mod_bwd_workspace_size": (_S, [_I, _I, _I, _I]),
+    "fa_mod_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _F, _F, _P]),
+    "fa_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "fa_cache_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "fa_cache_decode_workspace_size": (_S, [_I, _I, _I, _I, _I, _I]),
+    "fa_cache_decode_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _I, _F, _F, _I, _I,
+                                 _P]),
     "fa_record_launch_events": (_I, [ctypes.POINTER(ctypes.c_void_p), _I]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_get_device_error": (_I, [_P]),
@@ -339,5 +349,9 @@ def check_device_error(stream: Optional[torch.cuda.Stream] = None):
 
 
 from .autograd import attention, varlen_attention, pack, unpack  # noqa: E402
+from .modified import MaskPlan, mask_plan, mod_attention, mod_bwd, mod_bwd_workspace_size, mod_fwd  # noqa: E402
+from .cache import cache_append, cache_decode_fwd, cache_decode_workspace_size, cache_read  # noqa: E402
 
-__all__ += ["attention", "varlen_attention", "pack", "unpack"]
+__all__ += ["attention", "varlen_attention", "pack", "unpack", "MaskPlan", "mask_plan", "mod_fwd", "mod_bwd",
+            "mod_bwd_workspace_size", "mod_attention", "cache_append", "cache_read", "cache_decode_fwd",
+            "cache_decode_workspace_size"]

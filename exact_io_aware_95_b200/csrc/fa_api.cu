@@ -12,9 +12,14 @@
 
 #include "fa_bwd.cuh"
 #include "fa_bwd_dq.cuh"
+#include "fa_cache.cuh"
+#include "fa_cache_decode.cuh"
 #include "fa_decode.cuh"
 #include "fa_fwd.cuh"
 #include "fa_fwd_fp8.cuh"
+#include "fa_mod_bwd.cuh"
+#include "fa_mod_fwd.cuh"
+#include "fa_plan.cuh"
 
 namespace {
 
@@ -149,9 +154,9 @@ fa_status make_map_bf16(CUtensorMap* m, const void* base, int d, int H, int64_t 
 
 // Tensor map over a byte array (e4m3) with dims {d0, d1, d2, d3} (d0
 // innermost, contiguous), row pitches in bytes, boxes {b0, b1, b2, 1} and
-// 128-byte swizzle.
+// 128-byte swizzle (64-byte when asked for).
 fa_status make_map_u8(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const uint64_t (&pitch)[3],
-                      const uint32_t (&box)[3]) {
+                      const uint32_t (&box)[3], CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return FA_ERR_CUDA;
   cuuint64_t gd[4] = {dims[0], dims[1], dims[2], dims[3]};
@@ -159,7 +164,7 @@ fa_status make_map_u8(CUtensorMap* m, const void* base, const uint64_t (&dims)[4
   cuuint32_t bx[4] = {box[0], box[1], box[2], 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), gd, gs, bx, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
@@ -451,6 +456,151 @@ bool valid_cu(const int* cu, int nseq, int total, int max_seqlen) {
   return cu && nseq >= 1 && total >= 1 && max_seqlen >= 1;
 }
 
+// ---------------------------------------------------------------- mask plan
+struct PlanLayout {
+  size_t rows, qt, kt, total;
+};
+PlanLayout plan_layout(int64_t B, int64_t N) {
+  const size_t T = static_cast<size_t>((N + 127) / 128);
+  PlanLayout l;
+  l.rows = 0;
+  l.qt = align256(static_cast<size_t>(B) * N * sizeof(int2));
+  l.kt = l.qt + align256(B * T * sizeof(fa::PlanQTile));
+  l.total = l.kt + align256(B * T * sizeof(fa::PlanKTile));
+  return l;
+}
+fa::PlanView plan_view(const void* plan, int B, int N) {
+  const PlanLayout l = plan_layout(B, N);
+  char* p = static_cast<char*>(const_cast<void*>(plan));
+  fa::PlanView v;
+  v.rows = reinterpret_cast<int2*>(p + l.rows);
+  v.qt = reinterpret_cast<fa::PlanQTile*>(p + l.qt);
+  v.kt = reinterpret_cast<fa::PlanKTile*>(p + l.kt);
+  return v;
+}
+// Limits shared by the modified-score calls: positions and tile indexes fit
+// 32 bits with room for the window and tile arithmetic.
+bool valid_plan_shape(int B, int N) { return B >= 1 && N >= 1 && N <= (1 << 24); }
+
+// ------------------------------------------------- modified-score attention
+fa_status mod_check(int B, int N, int H, int Hkv, int d, float scale, float softcap, const void* plan,
+                    const float* slopes) {
+  if (!valid_plan_shape(B, N) || H < 1 || Hkv < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) != 0) return FA_ERR_INVALID_ARG;
+  if (slopes && (reinterpret_cast<uintptr_t>(slopes) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return FA_ERR_INVALID_ARG;
+  // scale / softcap and softcap * log2(e) must be representable
+  if (softcap > 0.f && (!std::isfinite(scale / softcap) || !std::isfinite(softcap * kLog2e))) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * N > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * N * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+template <int D, bool CAP, bool BIAS>
+fa_status launch_mod_fwd(int dev, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                         const fa::ModFwdParams& p, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  auto kern = fa::fa_mod_fwd_kernel<D, CAP, BIAS>;
+  constexpr int smem = fa::FwdCfg<D>::SMEM_BYTES;
+  fa_status st = ensure_smem(kern, dev, smem, done, fa::kLaunchRegs);
+  if (st != FA_OK) return st;
+  const int64_t grid = static_cast<int64_t>(p.npairs) * p.B * p.H;
+  if (grid <= 0 || grid > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  mark_launch(s);
+  kern<<<static_cast<unsigned>(grid), fa::FwdCfg<D>::THREADS, smem, s>>>(q, k, v, p);
+  return launch_status(s);
+}
+
+template <int D>
+fa_status dispatch_mod_fwd(int dev, bool cap, bool bias, const CUtensorMap& q, const CUtensorMap& k,
+                           const CUtensorMap& v, const fa::ModFwdParams& p, cudaStream_t s) {
+  if (cap) return bias ? launch_mod_fwd<D, true, true>(dev, q, k, v, p, s) : launch_mod_fwd<D, true, false>(dev, q, k, v, p, s);
+  return bias ? launch_mod_fwd<D, false, true>(dev, q, k, v, p, s) : launch_mod_fwd<D, false, false>(dev, q, k, v, p, s);
+}
+
+template <int D, bool CAP, bool BIAS>
+fa_status launch_mod_bwd(int dev, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                         const CUtensorMap& mdo, const fa::ModBwdParams& p, const fa::BwdParams& conv, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  auto kern = fa::fa_mod_bwd_kernel<D, CAP, BIAS>;
+  constexpr int smem = fa::ModBwdCfg<D>::SMEM_BYTES;
+  fa_status st = ensure_smem(kern, dev, smem, done, fa::BwdCfg<D>::LAUNCH_REGS);
+  if (st != FA_OK) return st;
+  const int64_t grid = static_cast<int64_t>(p.T) * p.B * p.Hkv;
+  const int64_t blocks = static_cast<int64_t>(p.B) * p.H * ((p.N + 31) / 32);
+  if (grid > 0x7fffffff || blocks > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  mark_launch(s);
+  fa::fa_mod_bwd_preprocess_kernel<D><<<preprocess_blocks(dev), 256, 0, s>>>(p);
+  if ((st = launch_status(s)) != FA_OK) return st;
+  kern<<<static_cast<unsigned>(grid), fa::BwdCfg<D>::THREADS, smem, s>>>(mq, mk, mv, mdo, p);
+  if ((st = launch_status(s)) != FA_OK) return st;
+  fa::fa_bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(conv);
+  return launch_status(s);
+}
+
+template <int D>
+fa_status dispatch_mod_bwd(int dev, bool cap, bool bias, const CUtensorMap& q, const CUtensorMap& k,
+                           const CUtensorMap& v, const CUtensorMap& d_o, const fa::ModBwdParams& p,
+                           const fa::BwdParams& conv, cudaStream_t s) {
+  if (cap)
+    return bias ? launch_mod_bwd<D, true, true>(dev, q, k, v, d_o, p, conv, s)
+                : launch_mod_bwd<D, true, false>(dev, q, k, v, d_o, p, conv, s);
+  return bias ? launch_mod_bwd<D, false, true>(dev, q, k, v, d_o, p, conv, s)
+              : launch_mod_bwd<D, false, false>(dev, q, k, v, d_o, p, conv, s);
+}
+
+// ------------------------------------------------------------- 8-bit cache
+// Tokens per block: about 64 (token, head) rows, at least one token.
+int cache_tokens_per_block(int Hkv) { return Hkv >= 64 ? 1 : 64 / Hkv; }
+
+fa_status cache_check(int B, int Nk, int Hkv, int d) {
+  if (B < 1 || Nk < 1 || Hkv < 1 || B > 65535) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * Nk * Hkv * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
+  // row indexes of one entry's token chunk and the exponent plane fit 32 bits
+  if (static_cast<int64_t>(Nk) * Hkv > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+struct CacheDecodeWs {
+  size_t prefix, bad, rec_o, rec_lse, total;
+};
+CacheDecodeWs cache_decode_ws(int B, int d) {
+  CacheDecodeWs w;
+  const size_t recs = static_cast<size_t>(fa::kCacheDecodeGrid) * 2 * 16;
+  w.prefix = 0;
+  w.bad = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
+  w.rec_o = w.bad + 256;
+  w.rec_lse = w.rec_o + align256(recs * d * sizeof(float));
+  w.total = w.rec_lse + align256(recs * sizeof(float));
+  return w;
+}
+
+template <int D, bool CAP, bool BIAS>
+fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap& mv, const fa::CDecParams& p,
+                              cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  auto kern = fa::fa_cache_decode_kernel<D, CAP, BIAS>;
+  constexpr int smem = fa::CDecCfg<D>::SMEM_BYTES;
+  fa_status st = ensure_smem(kern, dev, smem, done);
+  if (st != FA_OK) return st;
+  mark_launch(s);
+  kern<<<static_cast<unsigned>(p.grid), fa::CDecCfg<D>::THREADS, smem, s>>>(mk, mv, p);
+  if ((st = launch_status(s)) != FA_OK) return st;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.Nq;
+  fa::fa_cache_decode_merge_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(p, D);
+  return launch_status(s);
+}
+
+template <int D>
+fa_status dispatch_cache_decode(int dev, bool cap, bool bias, const CUtensorMap& mk, const CUtensorMap& mv,
+                                const fa::CDecParams& p, cudaStream_t s) {
+  if (cap)
+    return bias ? launch_cache_decode<D, true, true>(dev, mk, mv, p, s) : launch_cache_decode<D, true, false>(dev, mk, mv, p, s);
+  return bias ? launch_cache_decode<D, false, true>(dev, mk, mv, p, s) : launch_cache_decode<D, false, false>(dev, mk, mv, p, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -627,6 +777,255 @@ fa_status fa_fwd_fp8(const void* q, const void* k, const void* v, float descale_
   if (grid > 0x7fffffff) return FA_ERR_INVALID_ARG;
   kern<<<static_cast<unsigned>(grid), fa::Fp8Cfg::THREADS, smem, s>>>(mq, mk, mvt, p);
   return launch_status(s);
+}
+
+size_t fa_mask_plan_size(int B, int N) { return valid_plan_shape(B, N) ? plan_layout(B, N).total : 0; }
+
+fa_status fa_mask_plan(void* plan, size_t plan_bytes, const int* doc_ids, const int* prefix_len, int B, int N,
+                       int window, int causal, void* stream) {
+  LaunchEventsScope hook_scope;
+  if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) != 0) return FA_ERR_INVALID_ARG;
+  if (!valid_plan_shape(B, N) || window < 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * N > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(doc_ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(prefix_len) & 3u) != 0)
+    return FA_ERR_INVALID_ARG;
+  if (plan_bytes < plan_layout(B, N).total) return FA_ERR_WORKSPACE;
+  int dev;
+  fa_status st = current_device(&dev);
+  if (st != FA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  mark_launch(s);
+  fa::fa_mask_plan_kernel<<<static_cast<unsigned>(B), fa::kPlanThreads, 0, s>>>(plan_view(plan, B, N), doc_ids,
+                                                                                prefix_len, N, window, causal);
+  return launch_status(s);
+}
+
+fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void* o_low, float* lse, const void* plan,
+                     const float* slopes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
+                     void* stream) {
+  LaunchEventsScope hook_scope;
+  const void* ptrs[] = {q, k, v, o, lse};
+  for (const void* ptr : ptrs)
+    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(o_low)) return FA_ERR_INVALID_ARG;
+  int dev;
+  fa_status st = mod_check(B, N, H, Hkv, d, scale, softcap, plan, slopes);
+  if (st != FA_OK || (st = current_device(&dev)) != FA_OK) return st;
+  CUtensorMap mq, mk, mv;
+  if ((st = make_map_bf16(&mq, q, d, H, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mk, k, d, Hkv, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mv, v, d, Hkv, N, B, 128)) != FA_OK) return st;
+  fa::ModFwdParams p;
+  p.o = o;
+  p.o_low = o_low;
+  p.lse = lse;
+  p.slopes = slopes;
+  p.plan = plan_view(plan, B, N);
+  p.B = B;
+  p.N = N;
+  p.H = H;
+  p.G = H / Hkv;
+  p.T = (N + 127) / 128;
+  p.npairs = (N + 255) / 256;
+  // K and V of one head; the heads of a group share theirs
+  p.group = head_group((static_cast<int64_t>(N) * d * 2 * 2 + p.G - 1) / p.G, static_cast<int64_t>(B) * H);
+  p.scale_log2 = scale * kLog2e;
+  p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
+  p.cap_log2 = softcap * kLog2e;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return d == 64 ? dispatch_mod_fwd<64>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, p, s)
+                 : dispatch_mod_fwd<128>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, p, s);
+}
+
+size_t fa_mod_bwd_workspace_size(int B, int N, int H, int d) {
+  if (!valid_plan_shape(B, N)) return 0;
+  return fa_bwd_workspace_size(B, N, H, d);
+}
+
+fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o, const void* o_low, const float* lse,
+                     const void* dO, void* dq, void* dk, void* dv, const void* plan, const float* slopes,
+                     void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
+                     void* stream) {
+  LaunchEventsScope hook_scope;
+  const void* ptrs[] = {q, k, v, o, lse, dO, dq, dk, dv, workspace};
+  for (const void* ptr : ptrs)
+    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(o_low) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_INVALID_ARG;
+  int dev;
+  fa_status st = mod_check(B, N, H, Hkv, d, scale, softcap, plan, slopes);
+  if (st != FA_OK) return st;
+  if (ws_bytes < ws_bytes_for(static_cast<int64_t>(B) * N, H, d)) return FA_ERR_WORKSPACE;
+  if ((st = current_device(&dev)) != FA_OK) return st;
+  CUtensorMap mq, mk, mv, mdo;
+  if ((st = make_map_bf16(&mq, q, d, H, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mk, k, d, Hkv, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mv, v, d, Hkv, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mdo, dO, d, H, N, B, 128)) != FA_OK) return st;
+  fa::ModBwdParams p;
+  p.o = o;
+  p.o_low = o_low;
+  p.dout = dO;
+  p.lse = lse;
+  p.slopes = slopes;
+  p.dk = dk;
+  p.dv = dv;
+  p.dq_acc = static_cast<float*>(workspace);
+  p.dvec = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                    align256(static_cast<size_t>(B) * N * H * d * sizeof(float)));
+  p.plan = plan_view(plan, B, N);
+  p.B = B;
+  p.N = N;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = H / Hkv;
+  p.T = (N + 127) / 128;
+  p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.G, static_cast<int64_t>(B) * Hkv);  // Q, dO, dQ acc
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
+  p.cap_log2 = softcap * kLog2e;
+  fa::BwdParams conv = {};  // what the dQ conversion reads
+  conv.dq = dq;
+  conv.dq_acc = p.dq_acc;
+  conv.N = N;
+  conv.H = H;
+  conv.scale = scale;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return d == 64 ? dispatch_mod_bwd<64>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, mdo, p, conv, s)
+                 : dispatch_mod_bwd<128>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, mdo, p, conv, s);
+}
+
+fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                          const int* start, const int* count, int B, int T, int Nk, int Hkv, int d, void* stream) {
+  LaunchEventsScope hook_scope;
+  const void* ptrs[] = {k, v, k_cache, v_cache};
+  for (const void* ptr : ptrs)
+    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!k_scale || !v_scale || !start) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(start) & 3u) != 0 || (reinterpret_cast<uintptr_t>(count) & 3u) != 0)
+    return FA_ERR_INVALID_ARG;
+  if (T < 1 || T > Nk) return FA_ERR_INVALID_ARG;
+  int dev;
+  fa_status st = cache_check(B, Nk, Hkv, d);
+  if (st != FA_OK || (st = current_device(&dev)) != FA_OK) return st;
+  fa::CacheAppendParams p;
+  p.k = k;
+  p.v = v;
+  p.kcodes = static_cast<uint8_t*>(k_cache);
+  p.vcodes = static_cast<uint8_t*>(v_cache);
+  p.kexp = static_cast<uint8_t*>(k_scale);
+  p.vexp = static_cast<uint8_t*>(v_scale);
+  p.start = start;
+  p.count = count;
+  p.T = T;
+  p.Nk = Nk;
+  p.Hkv = Hkv;
+  p.tb = cache_tokens_per_block(Hkv);
+  const dim3 grid((T + p.tb - 1) / p.tb, B, 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  mark_launch(s);
+  if (d == 64) fa::fa_cache_append_kernel<64><<<grid, 256, 0, s>>>(p);
+  else fa::fa_cache_append_kernel<128><<<grid, 256, 0, s>>>(p);
+  return launch_status(s);
+}
+
+fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens, void* out, int B, int Nk, int Hkv,
+                        int d, void* stream) {
+  LaunchEventsScope hook_scope;
+  if (!cache || !scale || !out || !aligned16(cache) || !aligned16(out)) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(seqlens) & 3u) != 0) return FA_ERR_INVALID_ARG;
+  int dev;
+  fa_status st = cache_check(B, Nk, Hkv, d);
+  if (st != FA_OK || (st = current_device(&dev)) != FA_OK) return st;
+  fa::CacheReadParams p;
+  p.codes = static_cast<const uint8_t*>(cache);
+  p.exps = static_cast<const uint8_t*>(scale);
+  p.seqlens = seqlens;
+  p.out = out;
+  p.Nk = Nk;
+  p.Hkv = Hkv;
+  p.tb = cache_tokens_per_block(Hkv);
+  const dim3 grid((Nk + p.tb - 1) / p.tb, B);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  mark_launch(s);
+  if (d == 64) fa::fa_cache_read_kernel<64><<<grid, 256, 0, s>>>(p);
+  else fa::fa_cache_read_kernel<128><<<grid, 256, 0, s>>>(p);
+  return launch_status(s);
+}
+
+size_t fa_cache_decode_workspace_size(int B, int Nq, int Nk, int H, int Hkv, int d) {
+  if (B < 1 || B > 65535 || Nq < 1 || Nq > 16 || Nk < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128))
+    return 0;
+  return cache_decode_ws(B, d).total;
+}
+
+fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                              const void* v_scale, void* o, float* lse, const int* seqlens_k, const float* slopes,
+                              void* workspace, size_t ws_bytes, int B, int Nq, int Nk, int H, int Hkv, int d,
+                              float scale, float softcap, int window, int causal, void* stream) {
+  LaunchEventsScope hook_scope;
+  const void* ptrs[] = {q, k_cache, v_cache, o, lse};
+  for (const void* ptr : ptrs)
+    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!k_scale || !v_scale) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(seqlens_k) & 3u) != 0 || (reinterpret_cast<uintptr_t>(slopes) & 3u) != 0)
+    return FA_ERR_INVALID_ARG;
+  if (Nq < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || window < 0) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return FA_ERR_INVALID_ARG;
+  if (softcap > 0.f && (!std::isfinite(scale / softcap) || !std::isfinite(softcap * kLog2e))) return FA_ERR_INVALID_ARG;
+  if (Nq > 16) return FA_ERR_UNSUPPORTED;
+  fa_status st = cache_check(B, Nk, Hkv, d);
+  if (st != FA_OK) return st;
+  if (Nk > (1 << 30) || static_cast<int64_t>(B) * Nq * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
+  if ((static_cast<int64_t>(B) * Nq * H + 3) / 4 > 0x7fffffff || static_cast<int64_t>(H) * Nq > 0x7fffffff)
+    return FA_ERR_INVALID_ARG;
+  const CacheDecodeWs wl = cache_decode_ws(B, d);
+  if (!workspace || ws_bytes < wl.total) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_INVALID_ARG;
+  int dev;
+  if ((st = current_device(&dev)) != FA_OK) return st;
+  CUtensorMap mk, mv;
+  {
+    const uint64_t row = static_cast<uint64_t>(d);
+    const uint64_t dims[4] = {row, static_cast<uint64_t>(Hkv), static_cast<uint64_t>(Nk), static_cast<uint64_t>(B)};
+    const uint64_t pitch[3] = {row, row * Hkv, row * Hkv * Nk};
+    const uint32_t box[3] = {static_cast<uint32_t>(d), 1, 32};
+    const CUtensorMapSwizzle sw = d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if ((st = make_map_u8(&mk, k_cache, dims, pitch, box, sw)) != FA_OK) return st;
+    if ((st = make_map_u8(&mv, v_cache, dims, pitch, box, sw)) != FA_OK) return st;
+  }
+  fa::CDecParams p;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.kexp = static_cast<const uint8_t*>(k_scale);
+  p.vexp = static_cast<const uint8_t*>(v_scale);
+  p.seqlens = seqlens_k;
+  p.slopes = slopes;
+  char* ws = static_cast<char*>(workspace);
+  p.prefix = reinterpret_cast<long long*>(ws + wl.prefix);
+  p.bad = reinterpret_cast<int*>(ws + wl.bad);
+  p.rec_o = reinterpret_cast<float*>(ws + wl.rec_o);
+  p.rec_lse = reinterpret_cast<float*>(ws + wl.rec_lse);
+  p.B = B;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = H / Hkv;
+  p.rows = p.G * Nq;
+  p.nrb = (p.rows + 15) / 16;
+  p.grid = fa::kCacheDecodeGrid;
+  p.causal = causal;
+  p.window = window;
+  p.scale_log2 = scale * kLog2e;
+  p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
+  p.cap_log2 = softcap * kLog2e;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return d == 64 ? dispatch_cache_decode<64>(dev, softcap > 0.f, slopes != nullptr, mk, mv, p, s)
+                 : dispatch_cache_decode<128>(dev, softcap > 0.f, slopes != nullptr, mk, mv, p, s);
 }
 
 fa_status fa_record_launch_events(void* const* events, int n) {

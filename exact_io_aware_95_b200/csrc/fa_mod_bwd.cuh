@@ -1,0 +1,716 @@
+// Modified-score attention, backward, for sm_100a.  With the notation of
+// fa_mod_fwd.cuh and t_ij = tanh(x_ij / cap):
+//
+//     P_ij  = exp(z_ij - LSE_i)                   recomputed, 0 outside the mask
+//     D_i   = sum_c dO_ic O_ic
+//     dP    = dO V^T
+//     dS_ij = P_ij (1 - t_ij^2) (dP_ij - D_i)     (the factor only with CAP)
+//     dV_j  = sum P_ij dO_i        over the queries and the heads of the group
+//     dK_j  = scale sum dS_ij q_i  likewise
+//     dQ_i  = scale sum dS_ij k_j
+//
+// Three launches, as in the plain backward (fa_bwd.cuh): D and the zeroed fp32
+// dQ accumulator; the fused main kernel; dQ to bf16.  The main kernel is the
+// plain one's pipeline (same warps, barriers, tensor-memory columns and
+// products, S^T form with one key per lane) with these differences:
+//   - a work item is (128-key tile, batch entry, key head); the CTA walks the
+//     query tiles of the mask plan's range for that key tile, for every query
+//     head of the group in turn, so dK and dV of a shared key head accumulate
+//     in tensor memory over the whole group: no atomics, no second pass, a
+//     fixed order.  A key tile no query sees is stored as zero;
+//   - D takes O with its rounding residual when the caller has it: with O in
+//     bf16 alone, rows that one key dominates (P near 1, dP - D near 0) lose
+//     bits: relative error of dQ 5.2e-3 against 3.0e-3 at q = 8 N(0,1),
+//     k = N(0,1), d = 64, N = 1024;
+//   - the row term of the exponent, -LSE_i log2 e, carries the query's part of
+//     a one-sided distance bias (the key's part is one constant per thread);
+//   - with CAP the thread keeps bf16(P (1 - t^2)) instead of bf16(P) for dS,
+//     so the extra factor costs no registers between the two phases.
+#pragma once
+#include "fa_bwd.cuh"
+#include "fa_mod_fwd.cuh"
+
+namespace fa {
+
+struct ModBwdParams {
+  const void* o;
+  const void* o_low;    // bf16 residual of O, or nullptr
+  const void* dout;
+  const float* lse;
+  const float* slopes;  // [H], BIAS
+  void* dk;
+  void* dv;
+  float* dq_acc;        // layout: dq_acc_index4()
+  float* dvec;          // fp32 D [B, H, N]
+  PlanView plan;
+  int B, N, H, Hkv, G;
+  int T;                // ceil(N / 128)
+  int group;            // key heads per scheduling group
+  float scale, scale_log2, x_mul, cap_log2;
+};
+
+// D = rowsum(dO (O + O_low)) and the zeroed dQ accumulator; the shape of
+// fa_bwd_preprocess_kernel.
+template <int D>
+__global__ void __launch_bounds__(256) fa_mod_bwd_preprocess_kernel(const ModBwdParams p) {
+  constexpr int LPR = D / 8;
+  constexpr int RPW = 32 / LPR;
+  const int64_t nthreads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t gtid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t nrows = static_cast<int64_t>(p.B) * p.N * p.H;
+  const int64_t nacc4 = nrows * (D / 4);
+  float4* acc = reinterpret_cast<float4*>(p.dq_acc);
+  for (int64_t i = gtid; i < nacc4; i += nthreads) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPR, part = lane % LPR;
+  const int64_t nwarps = nthreads >> 5;
+  constexpr int U = 4;  // warp steps whose loads are in flight together
+  for (int64_t w0 = (gtid >> 5) * U; w0 * RPW < nrows; w0 += nwarps * U) {
+    uint4 ov[U], gv[U], lv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = (w0 + u) * RPW + sub;
+      ov[u] = gv[u] = lv[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < nrows) {
+        const size_t off = static_cast<size_t>(row) * D + part * 8;
+        ov[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.o) + off);
+        gv[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.dout) + off);
+        if (p.o_low) lv[u] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.o_low) + off);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = (w0 + u) * RPW + sub;
+      const uint32_t ow[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w}, gw[4] = {gv[u].x, gv[u].y, gv[u].z, gv[u].w},
+                     lw[4] = {lv[u].x, lv[u].y, lv[u].z, lv[u].w};
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum = fmaf(bf16lo_to_f32(ow[e]) + bf16lo_to_f32(lw[e]), bf16lo_to_f32(gw[e]), sum);
+        sum = fmaf(bf16hi_to_f32(ow[e]) + bf16hi_to_f32(lw[e]), bf16hi_to_f32(gw[e]), sum);
+      }
+#pragma unroll
+      for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (part == 0 && row < nrows) {
+        const int64_t tok = row / p.H;
+        const int h = static_cast<int>(row % p.H);
+        const int64_t b = tok / p.N, n = tok % p.N;
+        p.dvec[(static_cast<size_t>(b) * p.H + h) * p.N + n] = sum;
+      }
+    }
+  }
+}
+
+template <int D>
+struct ModBwdCfg : BwdCfg<D> {
+  using Base = BwdCfg<D>;
+  // visible key range of each query column, relative to the key tile:
+  // 128 words lo | len << 16 behind the D vector
+  static constexpr int OFF_SEE = Base::OFF_BAR;
+  static constexpr int OFF_BAR = OFF_SEE + 512;
+  static constexpr int OFF_MISC = (OFF_BAR + Base::NBAR * 8 + 15) & ~15;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+// One work item: (128-key tile j, batch entry, key head).  Key heads go in
+// groups of p.group, sized on the host so that a group's Q, dO and dQ
+// accumulator rows stay in L2; inside a group early key tiles go first (under
+// a causal mask they meet the most queries).
+struct ModBwdItem {
+  int hk, b, k0, i_begin, ni, niter;  // niter = ni query tiles x G heads
+};
+
+__device__ __forceinline__ void mod_bwd_item(const ModBwdParams& p, int c, ModBwdItem& it) {
+  const int nbh = p.B * p.Hkv;
+  const int g = c / (p.group * p.T);
+  const int gs = min(p.group, nbh - g * p.group);
+  const int cidx = c - g * p.group * p.T;
+  const int bh = g * p.group + cidx % gs;
+  const int j = cidx / gs;
+  it.hk = bh % p.Hkv;
+  it.b = bh / p.Hkv;
+  it.k0 = 128 * j;
+  const PlanKTile kt = p.plan.kt[static_cast<size_t>(it.b) * p.T + j];
+  it.i_begin = kt.qbeg;
+  it.ni = kt.qend - kt.qbeg;
+  it.niter = it.ni * p.G;
+}
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(512, 1)
+    fa_mod_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                  const ModBwdParams p) {
+  using C = ModBwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + C::MISC_ABORT);
+  volatile int* item_ring = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + C::MISC_ITEM);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + C::MISC_TMEM);
+  const uint32_t resp = sbase + C::OFF_MISC + C::MISC_RESP;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::BAR_KV), 1);
+    for (int s = 0; s < C::NSTAGE; ++s) {
+      mbar_init(bar(C::BAR_QDO_FULL + s), 1);
+      mbar_init(bar(C::BAR_QDO_EMPTY + s), 1);
+    }
+    mbar_init(bar(C::BAR_S), 1);
+    mbar_init(bar(C::BAR_DP), 1);
+    mbar_init(bar(C::BAR_P), 256);
+    mbar_init(bar(C::BAR_DS), 256);
+    mbar_init(bar(C::BAR_DS_EMPTY), 1);
+    mbar_init(bar(C::BAR_DQ_FULL), 1);
+    mbar_init(bar(C::BAR_DQ_EMPTY), 128);
+    mbar_init(bar(C::BAR_ACC), 1);
+    mbar_init(bar(C::BAR_DRAIN), 1);
+    mbar_init(bar(C::BAR_KV_EMPTY), 1);
+    mbar_init(bar(C::BAR_ACC_FREE), 256);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(bar(C::BAR_ITEM_FULL + k), 1);
+      mbar_init(bar(C::BAR_ITEM_EMPTY + k), C::ITEM_CONSUMERS);
+    }
+    mbar_init(bar(C::BAR_CLC), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Item n of this CTA from the two-slot ring the producer fills; -1 ends.
+  auto take_item = [&](int n, bool& ok) -> int {
+    const int slot = n & 1;
+    ok = mbar_wait(bar(C::BAR_ITEM_FULL + slot), (n >> 1) & 1, abort_flag);
+    if (!ok) return -1;
+    const int item = item_ring[slot];
+    mbar_arrive(bar(C::BAR_ITEM_EMPTY + slot));
+    return item;
+  };
+  if (warp >= 12) {
+    regs_set<C::REGS_PRODUCER, C::LAUNCH_REGS>();
+  }
+  if (warp == 12) {
+    // ------------------------------------------------------------ producer and scheduler
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmdO);
+      int item = blockIdx.x;
+      int nitems = 0;  // items whose K, V were loaded
+      int gt = 0;      // Q/dO tiles loaded (all items)
+      uint32_t clc_phase = 0;
+      bool clc_pending = false;
+      bool ok = true;
+      for (int n = 0; ok;) {
+        const int slot = n & 1;
+        if (n >= 2 && !(ok = mbar_wait(bar(C::BAR_ITEM_EMPTY + slot), ((n >> 1) - 1) & 1, abort_flag))) break;
+        item_ring[slot] = item;
+        mbar_arrive(bar(C::BAR_ITEM_FULL + slot));
+        ++n;
+        if (item < 0) break;
+        ModBwdItem I;
+        mod_bwd_item(p, item, I);
+        // ask for the next item now; the answer is read once this item's loads are issued
+        mbar_arrive_expect_tx(bar(C::BAR_CLC), 16);
+        clc_try_cancel(resp, bar(C::BAR_CLC));
+        clc_pending = true;
+        if (I.niter > 0) {
+          // K_j, V_j replace the previous item's once its products are done
+          if (nitems > 0 && !(ok = mbar_wait(bar(C::BAR_KV_EMPTY), (nitems - 1) & 1, abort_flag))) break;
+          mbar_arrive_expect_tx(bar(C::BAR_KV), 2 * C::TILE_BYTES);
+          for (int c = 0; c < C::NCHUNK; ++c) {
+            tma_load_4d(sbase + C::OFF_K + c * 16384, &tmK, bar(C::BAR_KV), c * 64, I.hk, I.k0, I.b);
+            tma_load_4d(sbase + C::OFF_V + c * 16384, &tmV, bar(C::BAR_KV), c * 64, I.hk, I.k0, I.b);
+          }
+          ++nitems;
+          int h = I.hk * p.G, i = 0;  // query head and tile of the walk
+          for (int it = 0; it < I.niter; ++it, ++gt) {
+            const int st = gt % C::NSTAGE;
+            const uint32_t ph = (gt / C::NSTAGE) & 1;
+            if (!(ok = mbar_wait(bar(C::BAR_QDO_EMPTY + st), ph ^ 1u, abort_flag))) break;
+            const int q0 = 128 * (I.i_begin + i);
+            mbar_arrive_expect_tx(bar(C::BAR_QDO_FULL + st), 2 * C::TILE_BYTES);
+            for (int c = 0; c < C::NCHUNK; ++c) {
+              tma_load_4d(sbase + C::OFF_Q + st * C::TILE_BYTES + c * 16384, &tmQ, bar(C::BAR_QDO_FULL + st), c * 64,
+                          h, q0, I.b);
+              tma_load_4d(sbase + C::OFF_DO + st * C::TILE_BYTES + c * 16384, &tmdO, bar(C::BAR_QDO_FULL + st),
+                          c * 64, h, q0, I.b);
+            }
+            if (++i == I.ni) {
+              i = 0;
+              ++h;
+            }
+          }
+          if (!ok) break;
+        }
+        if (!(ok = mbar_wait(bar(C::BAR_CLC), clc_phase, abort_flag))) break;
+        clc_pending = false;
+        clc_phase ^= 1u;
+        item = clc_query(resp);
+      }
+      if (*abort_flag) {  // let the copies and the cancel request in flight land before the CTA exits
+        if (nitems > 0) mbar_wait_drain(bar(C::BAR_KV), (nitems - 1) & 1);
+        for (int i = 0; i < C::NSTAGE && i < gt; ++i) {
+          const int n = gt - 1 - i;
+          mbar_wait_drain(bar(C::BAR_QDO_FULL + n % C::NSTAGE), (n / C::NSTAGE) & 1);
+        }
+        if (clc_pending) mbar_wait_drain(bar(C::BAR_CLC), clc_phase);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 13) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdSq = idesc_bf16_f32(128, 128, false, false);  // S^T, dP^T
+      constexpr uint32_t kIdDV = idesc_bf16_f32(128, D, false, true);     // dV (A in TMEM), dK
+      constexpr uint32_t kIdDQ = idesc_bf16_f32(128, D, true, true);      // dQ: A = dS (MN-major view)
+      // operand descriptors, built once; per MMA only the start address moves
+      const uint64_t dK_k = sdesc_sw128(sbase + C::OFF_K, 16, 1024);        // K as K-major A of S^T
+      const uint64_t dV_k = sdesc_sw128(sbase + C::OFF_V, 16, 1024);        // V as K-major A of dP^T
+      const uint64_t dK_mn = sdesc_sw128(sbase + C::OFF_K, 16384, 1024);    // K as MN-major B of dQ
+      const uint64_t dS_k = sdesc_sw128(sbase + C::OFF_DS, 16, 1024);       // dS^T as K-major A of dK
+      const uint64_t dS_mn = sdesc_sw128(sbase + C::OFF_DS, 16384, 1024);   // dS as MN-major A of dQ
+      const uint64_t dQ0_k = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);       // Q stage 0, K-major B of S^T
+      const uint64_t dQ0_mn = sdesc_sw128(sbase + C::OFF_Q, 16384, 1024);   // Q stage 0, MN-major B of dK
+      const uint64_t dO0_k = sdesc_sw128(sbase + C::OFF_DO, 16, 1024);      // dO stage 0, K-major B of dP^T
+      const uint64_t dO0_mn = sdesc_sw128(sbase + C::OFF_DO, 16384, 1024);  // dO stage 0, MN-major B of dV
+      constexpr uint32_t kStageAdv = C::TILE_BYTES >> 4;
+      auto issue_s = [&](int gt) {  // S^T = K Q_gt^T
+        const uint64_t bq = dQ0_k + (gt % C::NSTAGE) * kStageAdv;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_ss(tmem + C::TM_S, sdesc_adv(dK_k, off), sdesc_adv(bq, off), kIdSq, kk > 0);
+        }
+        umma_commit(bar(C::BAR_S));
+      };
+      auto issue_dp = [&](int gt) {  // dP^T = V dO_gt^T
+        const uint64_t bo = dO0_k + (gt % C::NSTAGE) * kStageAdv;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_ss(tmem + C::TM_DP, sdesc_adv(dV_k, off), sdesc_adv(bo, off), kIdSq, kk > 0);
+        }
+        umma_commit(bar(C::BAR_DP));
+      };
+      // Order per query tile i:  dV(i)  S^T(i+1)  dK(i)  dQ(i)  dP^T(i+1).
+      // dP^T does not depend on P, so dP^T(i+1) is issued as soon as its
+      // columns are free (the P/dS warps have read dP^T(i) and, at d = 128,
+      // the drain has emptied dQ(i), which shares them): the P/dS warps then
+      // go from P^T(i+1) straight on to dS^T(i+1), and P^T(i+1) is computed
+      // while dK(i) and dQ(i) run.
+      int gt0 = 0;     // tiles of earlier items
+      int nitems = 0;  // items done
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int item = take_item(n, ok);
+        if (!ok || item < 0) break;
+        ModBwdItem I;
+        mod_bwd_item(p, item, I);
+        const int niter = I.niter;
+        if (niter == 0) continue;
+        if (!(ok = mbar_wait(bar(C::BAR_KV), nitems & 1, abort_flag))) break;
+        if (!(ok = mbar_wait(bar(C::BAR_QDO_FULL + gt0 % C::NSTAGE), (gt0 / C::NSTAGE) & 1, abort_flag))) break;
+        tc_fence_after();
+        issue_s(gt0);
+        // at d = 128 the first dP^T reuses the columns of the previous item's last dQ
+        if (C::DQ_ALIASES_DP && gt0 > 0) {
+          if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), (gt0 - 1) & 1, abort_flag))) break;
+          tc_fence_after();
+        }
+        issue_dp(gt0);
+        for (int it = 0; ok && it < niter; ++it) {
+          const int gt = gt0 + it;
+          const int st = gt % C::NSTAGE;
+          const uint32_t par = gt & 1;
+          const uint64_t q_mn = dQ0_mn + st * kStageAdv;
+          const uint64_t o_mn = dO0_mn + st * kStageAdv;
+          // dV += P^T dO   (A = P^T packed bf16 in tensor memory)
+          if (!(ok = mbar_wait(bar(C::BAR_P), par, abort_flag))) break;
+          if (it == 0 && nitems > 0) {  // the previous item's dK, dV have been read out
+            if (!(ok = mbar_wait(bar(C::BAR_ACC_FREE), (nitems - 1) & 1, abort_flag))) break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            // queries 16kk..16kk+15 of P^T: columns 8kk (first 64 queries) or 32 + 8kk (last 64)
+            umma_ts(tmem + C::TM_DV, tmem + C::TM_S + kk * 8 + (kk >= 4 ? 32 : 0), sdesc_adv(o_mn, kk * 2048), kIdDV,
+                    (it > 0 || kk > 0));
+          // S^T of the next query tile (P^T(i) was consumed by dV above, in issue order)
+          if (it + 1 < niter) {
+            const int st1 = (gt + 1) % C::NSTAGE;
+            if (!(ok = mbar_wait(bar(C::BAR_QDO_FULL + st1), ((gt + 1) / C::NSTAGE) & 1, abort_flag))) break;
+            tc_fence_after();
+            issue_s(gt + 1);
+          }
+          // dK += dS^T Q ;  dQ_i = dS K
+          if (!(ok = mbar_wait(bar(C::BAR_DS), par, abort_flag))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ss(tmem + C::TM_DK, sdesc_adv(dS_k, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_adv(q_mn, kk * 2048),
+                    kIdDV, (it > 0 || kk > 0));
+          if (!C::DQ_ALIASES_DP && gt > 0) {
+            if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), par ^ 1u, abort_flag))) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ss(tmem + C::TM_DQ, sdesc_adv(dS_mn, kk * 2048), sdesc_adv(dK_mn, kk * 2048), kIdDQ, kk > 0);
+          umma_commit(bar(C::BAR_QDO_EMPTY + st));
+          umma_commit(bar(C::BAR_DS_EMPTY));
+          umma_commit(bar(C::BAR_DQ_FULL));
+          // dP^T of the next query tile: the P/dS warps finished reading dP^T(i)
+          // before they signalled dS^T(i); at d = 128 its columns also hold dQ(i),
+          // so wait until the drain has loaded it (completion i of DQ_EMPTY)
+          if (it + 1 < niter) {
+            if (C::DQ_ALIASES_DP) {
+              if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), par, abort_flag))) break;
+              tc_fence_after();
+            }
+            issue_dp(gt + 1);
+          }
+        }
+        if (!ok) break;
+        umma_commit(bar(C::BAR_ACC));       // dK, dV of this item complete
+        umma_commit(bar(C::BAR_KV_EMPTY));  // and no product reads K, V any more
+        gt0 += niter;
+        ++nitems;
+      }
+      if (*abort_flag) {
+        umma_commit(bar(C::BAR_DRAIN));
+        mbar_wait_drain(bar(C::BAR_DRAIN), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ P^T and dS^T
+    regs_set<C::REGS_PDS, C::LAUNCH_REGS>();
+    const int w = warp >> 2;          // this warpgroup's query columns: 64w .. 64w+63
+    const int t = threadIdx.x & 127;  // key row within the tile == tensor-memory lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* sLSE = reinterpret_cast<float*>(smem + C::OFF_LSE);
+    float* sDv = reinterpret_cast<float*>(smem + C::OFF_DV);
+    uint32_t* sSee = reinterpret_cast<uint32_t*>(smem + C::OFF_SEE);
+    constexpr float kLog2e = 1.4426950408889634f;
+    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    int gt0 = 0;
+    int nitems = 0;
+    for (int n = 0;; ++n) {
+      bool ok;
+      const int item = take_item(n, ok);
+      if (!__all_sync(0xffffffffu, ok) || item < 0) break;
+      ModBwdItem I;
+      mod_bwd_item(p, item, I);
+      const int k0 = I.k0;
+      const int key = k0 + t;
+      const bool key_ok = key < p.N;
+      // The terms of this warpgroup's query columns, thread t < 64 those of
+      // column 64w + t of the tile starting at q0: -LSE in base 2 with the
+      // query's part of a one-sided bias, D, and the keys of this tile that
+      // the query sees.  Rows past the end get -LSE = -inf, so P is exactly 0.
+      // `side`: how the bias runs over the tile pair: below the diagonal (or
+      // no row sees past itself) +1, above it -1, both sides 0.
+      float lv = 0.f, dv = 0.f, slope = 0.f;
+      uint32_t sv = 0;
+      int side = 1;
+      bool full = true;
+      auto fetch = [&](int h, int q0) {
+        const PlanQTile qt = p.plan.qt[static_cast<size_t>(I.b) * p.T + (q0 >> 7)];
+        full = k0 >= qt.full_lo && k0 + 128 <= qt.full_hi;
+        if constexpr (BIAS) {
+          slope = p.slopes[h] * kLog2e;
+          side = (q0 >= k0 + 127 || !qt.ahead) ? 1 : (q0 + 127 <= k0 ? -1 : 0);
+        }
+        const int q = q0 + 64 * w + t;
+        lv = -INFINITY;
+        dv = 0.f;
+        sv = 0;
+        if (t < 64 && q < p.N) {
+          const size_t li = (static_cast<size_t>(I.b) * p.H + h) * p.N + q;
+          lv = -p.lse[li] * kLog2e;
+          dv = p.dvec[li];
+          if constexpr (BIAS) lv -= side * slope * static_cast<float>(q - k0);
+          const int2 x = p.plan.rows[static_cast<size_t>(I.b) * p.N + q];
+          const int lo = min(max(x.x - k0, 0), 128), hi = min(max(x.y - k0, 0), 128);
+          sv = lo | (max(hi - lo, 0) << 16);
+        }
+      };
+      int h = I.hk * p.G, i = 0;
+      if (I.niter > 0) fetch(h, 128 * I.i_begin);
+      for (int it = 0; it < I.niter; ++it) {
+        const uint32_t par = (gt0 + it) & 1;
+        const int q0 = 128 * (I.i_begin + i);
+        named_bar_sync(1 + w, 128);  // the warpgroup is done with the previous tile's values
+        if (t < 64) {
+          sLSE[64 * w + t] = lv;
+          sDv[64 * w + t] = dv;
+          sSee[64 * w + t] = sv;
+        }
+        named_bar_sync(1 + w, 128);
+        const bool tile_full = full;
+        const int tile_side = side;
+        const float tile_slope = slope;
+        if (++i == I.ni) {
+          i = 0;
+          ++h;
+        }
+        if (it + 1 < I.niter) fetch(h, 128 * (I.i_begin + i));  // lands during this tile
+        ok = mbar_wait(bar(C::BAR_S), par, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float4* sLSE4 = reinterpret_cast<const float4*>(sLSE);
+        const uint4* sSee4 = reinterpret_cast<const uint4*>(sSee);
+        // the key's part of a one-sided bias
+        const float kb = BIAS ? tile_side * tile_slope * static_cast<float>(t) : 0.f;
+        const uint64_t kb2 = f2_pack(kb, kb);
+        uint32_t pk[2][16];  // bf16 pairs of P, or of P (1 - t^2) with CAP
+#pragma unroll
+        for (int hc = 0; hc < 2; ++hc) {
+          const int cc = 2 * w + hc;  // 32-column chunk of the 128-column tile
+          uint32_t s[32];
+          tmem_ld32(lane_base + C::TM_S + 32 * cc, s);
+          tmem_wait_ld(s);
+          bool small = true;
+          if constexpr (CAP) {
+            float ax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              ax = fmax3(ax, fabsf(__uint_as_float(s[e])), fabsf(__uint_as_float(s[e + 1])));
+            small = __all_sync(0xffffffffu, ax * fabsf(p.x_mul) <= kTanhRange);
+          }
+          uint32_t pw[16];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const float4 l4 = sLSE4[8 * cc + m];
+            const int qa = 32 * cc + 4 * m;
+            uint64_t s01 = f2_pack(__uint_as_float(s[4 * m + 0]), __uint_as_float(s[4 * m + 1]));
+            uint64_t s23 = f2_pack(__uint_as_float(s[4 * m + 2]), __uint_as_float(s[4 * m + 3]));
+            uint64_t l01 = f2_pack(l4.x, l4.y), l23 = f2_pack(l4.z, l4.w);
+            if constexpr (BIAS) {
+              l01 = fadd2(l01, kb2);
+              l23 = fadd2(l23, kb2);
+              if (tile_side == 0) {  // both sides of the diagonal: |i - j| element by element
+                const float d0 = static_cast<float>(q0 + qa - key);
+                l01 = fsub2(l01, f2_pack(tile_slope * fabsf(d0), tile_slope * fabsf(d0 + 1.f)));
+                l23 = fsub2(l23, f2_pack(tile_slope * fabsf(d0 + 2.f), tile_slope * fabsf(d0 + 3.f)));
+              }
+            }
+            uint64_t z01, z23;
+            if constexpr (CAP) {
+              const uint64_t xm2 = f2_pack(p.x_mul, p.x_mul), cl2 = f2_pack(p.cap_log2, p.cap_log2);
+              s01 = fmul2(s01, xm2);
+              s23 = fmul2(s23, xm2);
+              if (small) {
+                s01 = tanh2_poly(s01);
+                s23 = tanh2_poly(s23);
+              } else {
+                float a, b;
+                f2_unpack(s01, a, b);
+                s01 = f2_pack(tanh_any(a), tanh_any(b));
+                f2_unpack(s23, a, b);
+                s23 = f2_pack(tanh_any(a), tanh_any(b));
+              }
+              z01 = ffma2(s01, cl2, l01);
+              z23 = ffma2(s23, cl2, l23);
+            } else {
+              z01 = ffma2(s01, c2, l01);
+              z23 = ffma2(s23, c2, l23);
+            }
+            float x0, x1, x2, x3;
+            f2_unpack(z01, x0, x1);
+            f2_unpack(z23, x2, x3);
+            float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+            if (!tile_full) {
+              const uint4 sw = sSee4[8 * cc + m];
+              if (static_cast<uint32_t>(t) - (sw.x & 0xffffu) >= (sw.x >> 16)) p0 = 0.f;
+              if (static_cast<uint32_t>(t) - (sw.y & 0xffffu) >= (sw.y >> 16)) p1 = 0.f;
+              if (static_cast<uint32_t>(t) - (sw.z & 0xffffu) >= (sw.z >> 16)) p2 = 0.f;
+              if (static_cast<uint32_t>(t) - (sw.w & 0xffffu) >= (sw.w >> 16)) p3 = 0.f;
+            }
+            pw[2 * m] = pack_bf16x2(p0, p1);
+            pw[2 * m + 1] = pack_bf16x2(p2, p3);
+            if constexpr (CAP) {  // P (1 - t^2)
+              const uint64_t one = f2_pack(1.f, 1.f), neg = f2_pack(-1.f, -1.f);
+              float a, b;
+              f2_unpack(fmul2(f2_pack(p0, p1), ffma2(fmul2(s01, neg), s01, one)), a, b);
+              pk[hc][2 * m] = pack_bf16x2(a, b);
+              f2_unpack(fmul2(f2_pack(p2, p3), ffma2(fmul2(s23, neg), s23, one)), a, b);
+              pk[hc][2 * m + 1] = pack_bf16x2(a, b);
+            } else {
+              pk[hc][2 * m] = pw[2 * m];
+              pk[hc][2 * m + 1] = pw[2 * m + 1];
+            }
+          }
+          // P^T (bf16) into the first half of this warpgroup's own S^T columns
+          tmem_st16(lane_base + C::TM_S + 64 * w + 16 * hc, pw);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(C::BAR_P));
+        // dS^T = P^T (dP^T - D)
+        ok = mbar_wait(bar(C::BAR_DP), par, abort_flag) && mbar_wait(bar(C::BAR_DS_EMPTY), par ^ 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t region = sbase + C::OFF_DS + w * 16384;  // queries 64w..64w+63
+        const float4* sDv4 = reinterpret_cast<const float4*>(sDv);
+#pragma unroll
+        for (int hc = 0; hc < 2; ++hc) {
+          const int cc = 2 * w + hc;
+          uint32_t dp[32];
+          tmem_ld32(lane_base + C::TM_DP + 32 * cc, dp);
+          tmem_wait_ld(dp);
+          uint32_t wv[16];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const float4 d4 = sDv4[8 * cc + m];
+            const uint32_t a0 = pk[hc][2 * m], a1 = pk[hc][2 * m + 1];
+            float d0, d1, d2, d3;
+            f2_unpack(fmul2(f2_pack(bf16lo_to_f32(a0), bf16hi_to_f32(a0)),
+                            fsub2(f2_pack(__uint_as_float(dp[4 * m + 0]), __uint_as_float(dp[4 * m + 1])),
+                                  f2_pack(d4.x, d4.y))), d0, d1);
+            f2_unpack(fmul2(f2_pack(bf16lo_to_f32(a1), bf16hi_to_f32(a1)),
+                            fsub2(f2_pack(__uint_as_float(dp[4 * m + 2]), __uint_as_float(dp[4 * m + 3])),
+                                  f2_pack(d4.z, d4.w))), d2, d3);
+            wv[2 * m] = pack_bf16x2(d0, d1);
+            wv[2 * m + 1] = pack_bf16x2(d2, d3);
+          }
+          // 32 queries -> 16-byte chunks hc*4 + 0..3 of this row in region w
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            st_shared_v4(region + sw128_offset(t, hc * 4 + u), wv[4 * u], wv[4 * u + 1], wv[4 * u + 2], wv[4 * u + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(C::BAR_DS));
+      }
+      if (!ok) break;
+      // this item's rows: warpgroup 0 stores dK (times scale), warpgroup 1 stores
+      // dV, then both hand the accumulator columns back to the next item
+      const bool any = I.niter > 0;  // else: a key tile no query sees, stored as zero
+      if (any) {
+        ok = mbar_wait(bar(C::BAR_ACC), nitems & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+      }
+      const size_t row = (static_cast<size_t>(I.b) * p.N + key) * p.Hkv + I.hk;
+      const uint32_t col = w ? C::TM_DV : C::TM_DK;
+      const float mul = w ? 1.f : p.scale;
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(w ? p.dv : p.dk) + row * D;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t a[32];
+        if (any) {
+          tmem_ld32(lane_base + col + 32 * cc, a);
+          tmem_wait_ld(a);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = 0u;
+        }
+        uint32_t wv[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          wv[i] = pack_bf16x2(__uint_as_float(a[2 * i]) * mul, __uint_as_float(a[2 * i + 1]) * mul);
+        if (key_ok) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            st_global_v4(dst + 32 * cc + 8 * u, wv[4 * u], wv[4 * u + 1], wv[4 * u + 2], wv[4 * u + 3]);
+        }
+      }
+      if (any) {
+        tc_fence_before();
+        mbar_arrive(bar(C::BAR_ACC_FREE));
+        gt0 += I.niter;
+        ++nitems;
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ dQ_i drain
+    regs_set<C::REGS_DRAIN, C::LAUNCH_REGS>();
+    const int t = threadIdx.x - 256;  // query row within the tile == tensor-memory lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int gt0 = 0;
+    for (int n = 0;; ++n) {
+      bool ok;
+      const int item = take_item(n, ok);
+      if (!__all_sync(0xffffffffu, ok) || item < 0) break;
+      ModBwdItem I;
+      mod_bwd_item(p, item, I);
+      {
+        int h = I.hk * p.G, i = 0;
+        for (int it = 0; it < I.niter; ++it) {
+          const uint32_t par = (gt0 + it) & 1;
+          const int q = 128 * (I.i_begin + i) + t;
+          ok = mbar_wait(bar(C::BAR_DQ_FULL), par, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // accumulator rows: (bh, float4 group g, r) with r consecutive across the warp
+          const int bh_ = I.b * p.H + h;
+          if (++i == I.ni) {
+            i = 0;
+            ++h;
+          }
+          float4* acc4 = reinterpret_cast<float4*>(p.dq_acc);
+          // The whole dQ_i row is loaded first and its tensor-memory columns are
+          // released at once (at d = 128 dP^T(i+1) reuses them); the atomics
+          // then run from registers.  Issuing atomics stalls once the memory
+          // pipeline backs up, so none may stand between dQ_i and dP^T(i+1).
+          uint32_t a[D / 32][32];
+#pragma unroll
+          for (int cg = 0; cg < D / 32; ++cg) tmem_ld32(lane_base + C::TM_DQ + 32 * cg, a[cg]);
+#pragma unroll
+          for (int cg = 0; cg < D / 32; ++cg) tmem_wait_ld(a[cg]);
+          tc_fence_before();
+          mbar_arrive(bar(C::BAR_DQ_EMPTY));
+          if (q < p.N) {
+#pragma unroll
+            for (int cg = 0; cg < D / 32; ++cg)
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                atomicAdd(acc4 + dq_acc_index4(bh_, 8 * cg + u, q, p.N, D),
+                          make_float4(__uint_as_float(a[cg][4 * u]), __uint_as_float(a[cg][4 * u + 1]),
+                                      __uint_as_float(a[cg][4 * u + 2]), __uint_as_float(a[cg][4 * u + 3])));
+                if (u & 1) {
+                  const long long t0 = clock64();
+                  while (clock64() - t0 < C::DQ_ATOMIC_PAUSE) {
+                  }
+                }
+              }
+          }
+        }
+        if (!ok) break;
+      }
+      gt0 += I.niter;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace fa

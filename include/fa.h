@@ -175,6 +175,99 @@ fa_status fa_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
                         const int* seqlens_k, void* workspace, size_t ws_bytes,
                         int B, int Nq, int Nk, int H, int d, float scale, int causal, void* stream);
 
+/* ---- Attention with modified scores -----------------------------------------
+ * Dense batches as fa_fwd, with four additions:
+ *   - grouped heads: k, v (and dk, dv) are [B, N, Hkv, d], Hkv divides H, and
+ *     query head h reads key head h / (H / Hkv);
+ *   - softcap > 0: the scores x = scale * q . k become
+ *     softcap * tanh(x / softcap); 0 leaves them as they are;
+ *   - slopes (fp32 [H] device array, or NULL): the score of query i and key j
+ *     is then lowered by slopes[h] * |i - j| (any finite slope);
+ *   - the keys each query sees come from a mask plan, not from a flag.
+ * A query that sees no key gets O = 0, LSE = -inf and no gradient; a key that
+ * no query sees gets dK = dV = 0.  K and V must be finite also in rows that
+ * are masked (padding): they enter products with weight 0. */
+
+/* Mask plan: for each query one interval of keys [lo, hi), from any of
+ *   doc_ids     int32 [B, N] or NULL: query i sees the keys of the run of equal
+ *               ids around it (packed documents; an id that comes back later is
+ *               another document); a negative id is padding, which sees nothing
+ *               and is seen by no other document;
+ *   causal      1: only keys j <= i, and
+ *   prefix_len  int32 [B] or NULL, with causal = 1: keys j < prefix_len[b] of
+ *               the query's document also where j > i (values are clamped to
+ *               [0, N]; no effect with causal = 0);
+ *   window      > 0: only keys |i - j| < window; 0: no window.
+ * `plan` is a device buffer of plan_bytes >= fa_mask_plan_size(B, N) bytes,
+ * 256-byte aligned, written on `stream` and read by fa_mod_fwd and fa_mod_bwd
+ * for batches of exactly this B and N: make it once per batch.  N <= 2^24,
+ * B * N < 2^31.  fa_mask_plan_size returns 0 for invalid sizes. */
+size_t fa_mask_plan_size(int B, int N);
+fa_status fa_mask_plan(void* plan, size_t plan_bytes, const int* doc_ids, const int* prefix_len, int B, int N,
+                       int window, int causal, void* stream);
+
+/* Forward.  q, o: bf16 [B, N, H, d]; k, v: bf16 [B, N, Hkv, d]; lse: fp32
+ * [B, H, N].  o_low: NULL, or a bf16 [B, N, H, d] output for what rounding O to
+ * bf16 lost, bf16(O - bf16(O)); passing it to fa_mod_bwd keeps the gradients
+ * exact to bf16 where one key takes most of a row's weight. */
+fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void* o_low, float* lse, const void* plan,
+                     const float* slopes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
+                     void* stream);
+
+/* Backward.  o, lse (and o_low, or NULL) as fa_mod_fwd returned them with the
+ * same plan, slopes, scale and softcap.  dq: bf16 [B, N, H, d]; dk, dv: bf16
+ * [B, N, Hkv, d], summed over the heads of the group.  workspace: ws_bytes >=
+ * fa_mod_bwd_workspace_size(B, N, H, d), 256-byte aligned.  dK and dV are
+ * bitwise reproducible; dQ is accumulated with fp32 atomics as in fa_bwd.
+ * The slopes are constants: they get no gradient. */
+size_t fa_mod_bwd_workspace_size(int B, int N, int H, int d);
+fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o, const void* o_low, const float* lse,
+                     const void* dO, void* dq, void* dk, void* dv, const void* plan, const float* slopes,
+                     void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
+                     void* stream);
+
+/* ---- 8-bit key/value cache ----------------------------------------------------
+ * A cache is e4m3 codes [B, Nk, Hkv, d] and one exponent byte per row,
+ * [B, Hkv, Nk] (E8M0: a byte e stands for 2^(e - 127), 255 for NaN); the cached
+ * value is code * 2^(e - 127).  d is 64 or 128.
+ *
+ * fa_cache_append quantises new rows k, v (bf16 [B, T, Hkv, d], 1 <= T <= Nk)
+ * into rows start[b] .. start[b] + count[b] - 1 of entry b (start: int32 [B];
+ * count: int32 [B] with values in [0, T], or NULL for T).  e is the smallest
+ * byte >= 1 with amax <= 448 * 2^(e - 127), amax over the row's finite values;
+ * codes round to nearest even.  NaN is stored as NaN, infinities as the largest
+ * code of their sign, and a row with no finite non-zero value has e = 127;
+ * finite values beyond +-1.875 * 2^127 are taken as that, so that no finite
+ * value reads back as an infinity.  No other row of the cache changes.  An entry whose rows do not fit the cache, or
+ * whose count is outside [0, T], is left unwritten and reported by
+ * fa_get_device_error() as FA_ERR_INVALID_ARG; the other entries are written.
+ *
+ * fa_cache_read writes the cached values as bf16 (exactly) to out
+ * [B, Nk, Hkv, d]: rows below seqlens[b] (int32 [B] in [0, Nk], or NULL for all
+ * Nk), zero in the rows from there on.  An entry with a length outside [0, Nk]
+ * is left unwritten and reported as above. */
+fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                          const int* start, const int* count, int B, int T, int Nk, int Hkv, int d, void* stream);
+fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens, void* out, int B, int Nk, int Hkv,
+                        int d, void* stream);
+
+/* Decode-shaped forward from an 8-bit cache: Nq new queries per entry
+ * (1 <= Nq <= 16), q, o: bf16 [B, Nq, H, d], lse: fp32 [B, H, Nq], against the
+ * first seqlens_k[b] cached rows (NULL: all Nk; 0 <= L <= Nk).  Query i is the
+ * token at position L - Nq + i.  Grouped heads, softcap and slopes as in
+ * fa_mod_fwd, with |position - j| as the distance; causal = 1: keys
+ * j <= position; window > 0: keys |position - j| < window.  A query that sees
+ * no key gets O = 0, LSE = -inf.  Rows that no query of the entry sees may hold
+ * anything.  Lengths outside [0, Nk] and errors as in fa_decode_fwd.
+ * workspace: ws_bytes >= fa_cache_decode_workspace_size(), 256-byte aligned (it
+ * depends on B and d only); calls that may run at the same time, captured ones
+ * among them, need workspaces of their own. */
+size_t fa_cache_decode_workspace_size(int B, int Nq, int Nk, int H, int Hkv, int d);
+fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                              const void* v_scale, void* o, float* lse, const int* seqlens_k, const float* slopes,
+                              void* workspace, size_t ws_bytes, int B, int Nq, int Nk, int H, int Hkv, int d,
+                              float scale, float softcap, int window, int causal, void* stream);
+
 /* Measurement hook (no counterpart in the method: it serves the roofline
  * measurement, which times the dominant kernel of a multi-kernel call on its
  * own).  events: n (1..8) cudaEvent_t handles, created by the caller on the
