@@ -568,7 +568,7 @@ struct CacheDecodeWs {
 };
 CacheDecodeWs cache_decode_ws(int B, int d) {
   CacheDecodeWs w;
-  const size_t recs = static_cast<size_t>(fa::kCacheDecodeGrid) * 2 * 16;
+  const size_t recs = static_cast<size_t>(fa::kCacheDecodeGridMax) * 2 * 16;
   w.prefix = 0;
   w.bad = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
   w.rec_o = w.bad + 256;
@@ -577,28 +577,46 @@ CacheDecodeWs cache_decode_ws(int B, int d) {
   return w;
 }
 
-template <int D, bool CAP, bool BIAS>
-fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap& mv, const fa::CDecParams& p,
-                              cudaStream_t s) {
+// The merge kernel is launched with programmatic stream serialisation: its
+// blocks may be placed while the stream kernel ends, and wait for its end
+// (griddepcontrol) before they read.
+template <int D, int NB, bool CAP, bool BIAS>
+fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap& mv, fa::CDecParams p, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  auto kern = fa::fa_cache_decode_kernel<D, CAP, BIAS>;
-  constexpr int smem = fa::CDecCfg<D>::SMEM_BYTES;
+  auto kern = fa::fa_cache_decode_kernel<D, NB, CAP, BIAS>;
+  constexpr int smem = fa::CDecCfg<D, NB>::SMEM_BYTES;
   fa_status st = ensure_smem(kern, dev, smem, done);
   if (st != FA_OK) return st;
+  p.rpb = 8 * NB;
+  p.nrb = (p.rows + p.rpb - 1) / p.rpb;
+  p.grid = fa::cdec_ctas_per_sm(NB) * 148;
   mark_launch(s);
-  kern<<<static_cast<unsigned>(p.grid), fa::CDecCfg<D>::THREADS, smem, s>>>(mk, mv, p);
+  kern<<<static_cast<unsigned>(p.grid), fa::CDecCfg<D, NB>::THREADS, smem, s>>>(mk, mv, p);
   if ((st = launch_status(s)) != FA_OK) return st;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.Nq;
-  fa::fa_cache_decode_merge_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(p, D);
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * p.Nq));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fa::fa_cache_decode_merge_kernel, p, D) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
   return launch_status(s);
 }
 
-template <int D>
+template <int D, int NB>
 fa_status dispatch_cache_decode(int dev, bool cap, bool bias, const CUtensorMap& mk, const CUtensorMap& mv,
                                 const fa::CDecParams& p, cudaStream_t s) {
   if (cap)
-    return bias ? launch_cache_decode<D, true, true>(dev, mk, mv, p, s) : launch_cache_decode<D, true, false>(dev, mk, mv, p, s);
-  return bias ? launch_cache_decode<D, false, true>(dev, mk, mv, p, s) : launch_cache_decode<D, false, false>(dev, mk, mv, p, s);
+    return bias ? launch_cache_decode<D, NB, true, true>(dev, mk, mv, p, s)
+                : launch_cache_decode<D, NB, true, false>(dev, mk, mv, p, s);
+  return bias ? launch_cache_decode<D, NB, false, true>(dev, mk, mv, p, s)
+              : launch_cache_decode<D, NB, false, false>(dev, mk, mv, p, s);
 }
 
 }  // namespace
@@ -979,7 +997,7 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
   fa_status st = cache_check(B, Nk, Hkv, d);
   if (st != FA_OK) return st;
   if (Nk > (1 << 30) || static_cast<int64_t>(B) * Nq * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
-  if ((static_cast<int64_t>(B) * Nq * H + 3) / 4 > 0x7fffffff || static_cast<int64_t>(H) * Nq > 0x7fffffff)
+  if (static_cast<int64_t>(B) * Nq * H > 0x7fffffff || static_cast<int64_t>(H) * Nq > 0x7fffffff)
     return FA_ERR_INVALID_ARG;
   const CacheDecodeWs wl = cache_decode_ws(B, d);
   if (!workspace || ws_bytes < wl.total) return FA_ERR_WORKSPACE;
@@ -1016,16 +1034,18 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.rows = p.G * Nq;
-  p.nrb = (p.rows + 15) / 16;
-  p.grid = fa::kCacheDecodeGrid;
   p.causal = causal;
   p.window = window;
   p.scale_log2 = scale * kLog2e;
   p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
   p.cap_log2 = softcap * kLog2e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d == 64 ? dispatch_cache_decode<64>(dev, softcap > 0.f, slopes != nullptr, mk, mv, p, s)
-                 : dispatch_cache_decode<128>(dev, softcap > 0.f, slopes != nullptr, mk, mv, p, s);
+  const bool cap = softcap > 0.f, bias = slopes != nullptr;
+  if (p.rows <= 8)
+    return d == 64 ? dispatch_cache_decode<64, 1>(dev, cap, bias, mk, mv, p, s)
+                   : dispatch_cache_decode<128, 1>(dev, cap, bias, mk, mv, p, s);
+  return d == 64 ? dispatch_cache_decode<64, 2>(dev, cap, bias, mk, mv, p, s)
+                 : dispatch_cache_decode<128, 2>(dev, cap, bias, mk, mv, p, s);
 }
 
 fa_status fa_record_launch_events(void* const* events, int n) {

@@ -11,25 +11,29 @@
 // head.  At 6.5 TB/s an SM receives a 256-byte key/value pair every ~11 clocks,
 // too little time to convert and multiply 256 codes per query row on the CUDA
 // cores, so both products are tensor-core ones (mma m16n8k16, fp16 operands,
-// fp32 sums): the G Nq query rows of a key head fill up to 16 rows.  tcgen05
-// is not used: its operands come from shared memory, where codes would have to
-// be written back as 16-bit values first, and its smallest M is four times the
-// rows there are.
+// fp32 sums), with the cache as the 16-row operand and the G Nq query rows of a
+// key head as the 8 columns (NB = 1) or two times 8 (NB = 2; more rows take
+// further passes over the cache).  tcgen05 is not used: its operands come from
+// shared memory, where codes would have to be written back as 16-bit values
+// first, and its smallest M is many times the rows there are.
 //   - e4m3 is exact in fp16.  A query row is scaled by a power of two to just
 //     under 2^15 and is then exact in fp16 down to 2^-24 (its 8 significant
 //     bits fit); row scale and key scale are applied to the fp32 score.
 //   - The weight of key j in the second product is w_ij = 2^(z_ij + ev_j - mo_i)
 //     in fp16 (error 2^-11 relative, an eighth of the output's rounding to bf16):
 //     the value row's exponent ev_j joins the weight's, with a running maximum
-//     mo_i of its own, so w <= 2^8 and the largest contribution keeps full
-//     precision whatever the spread of the value scales.  The row sum is taken
-//     of 2^(z_ij - m_i) unrounded in fp32.
+//     mo_i of its own, so the largest contribution keeps full precision whatever
+//     the spread of the value scales.  The row sum is taken of 2^(z_ij - m_i)
+//     unrounded in fp32.  Both maxima move only when a score exceeds them by
+//     more than 8 (w <= 2^8 fits fp16): a warp votes on that, and reduces a new
+//     maximum over its lanes only then, so most tiles need no shuffles.
 //   - Operand layout: a k-step may take the head dimensions, and the second
-//     product's output columns, in any order as long as both operands agree.
-//     Thread (g, t) of a warp takes 32 contiguous dimensions of key g for the
-//     scores and 16 contiguous dimensions of keys 2t, 2t+1, 2t+8, 2t+9 for the
-//     output: 16-byte shared-memory loads, conflict-free under TMA's 128-byte
-//     swizzle at d = 128; no transposition of V.
+//     product's rows, in any order as long as both operands agree.  Thread
+//     (g, t) of a warp takes D / 4 contiguous dimensions of keys g and g + 8 for
+//     the scores and D / 8 contiguous dimensions of keys 2t, 2t+1, 2t+8, 2t+9
+//     for the output: wide shared-memory loads, conflict-free under TMA's
+//     128-byte swizzle at d = 128, and no transposition of V.  The weights go
+//     from the score layout to the operand layout by movmatrix.
 //   - Each of the four compute warps owns 16 keys of a 64-key tile with its own
 //     running maxima, sums and output: no block-wide step per tile.  They are
 //     joined in shared memory at the end of a segment piece.
@@ -43,7 +47,10 @@
 
 namespace fa {
 
-constexpr int kCacheDecodeGrid = 2 * 148;
+// Stream CTAs: one wave.  NB = 1 fits three CTAs of 128 registers a thread on
+// an SM, NB = 2 two of 168.
+__host__ __device__ constexpr int cdec_ctas_per_sm(int NB) { return NB == 1 ? 3 : 2; }
+constexpr int kCacheDecodeGridMax = 3 * 148;
 
 struct CDecParams {
   const void* q;          // bf16 [B, Nq, H, d]
@@ -55,33 +62,34 @@ struct CDecParams {
   const float* slopes;    // [H] or nullptr
   long long* prefix;      // [B + 1] first unit of each entry, for the merge
   int* bad;
-  float* rec_o;           // [grid][2][16][d]
-  float* rec_lse;         // [grid][2][16]
+  float* rec_o;           // [grid][2][8 NB][d]
+  float* rec_lse;         // [grid][2][8 NB]
   int B, Nq, Nk, H, Hkv, G;
-  int rows, nrb;          // G Nq query rows per key head, blocks of 16
+  int rows, nrb, rpb;     // G Nq query rows per key head, blocks of rpb = 8 NB
   int grid, causal, window;
   float scale_log2;       // scale log2 e          (no cap)
   float x_mul, cap_log2;  // scale / cap, cap log2 e
 };
 
-template <int D>
+template <int D, int NB>
 struct CDecCfg {
   static constexpr int KT = 64;
   static constexpr int NW = 4;                     // compute warps, 16 keys of a tile each
+  static constexpr int R = 8 * NB;                 // query rows of a block
   static constexpr int TILE = KT * D;              // bytes of a K or V tile
-  static constexpr int NSTAGE = D == 128 ? 6 : 10;
+  static constexpr int NSTAGE = (NB == 1 ? 4 : 6) * 128 / D;
   static constexpr int OFF_KV = 0;
-  static constexpr int OFF_SC = OFF_KV + NSTAGE * 2 * TILE;   // float [NW][2][32] key and value scales
-  static constexpr int OFF_ML = OFF_SC + NW * 2 * 32 * 4;     // float [3][NW][16] m, mo, l
-  static constexpr int OFF_ACC = OFF_ML + 3 * NW * 16 * 4;    // float [NW][4][D + 4]
+  static constexpr int OFF_ML = OFF_KV + NSTAGE * 2 * TILE;   // float [3][NW][R] m, mo, l
+  static constexpr int OFF_ACC = OFF_ML + 3 * NW * R * 4;     // float [NW][4][D + 4]
   static constexpr int ACC_LD = D + 4;
   static constexpr int OFF_BAR = OFF_ACC + NW * 4 * ACC_LD * 4;
   static constexpr int BAR_FULL = 0, BAR_EMPTY = NSTAGE, NBAR = 2 * NSTAGE;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  // misc: abort flag | bad | scan [8] | b0 | base of b0 (8 bytes) | U (8 bytes)
-  static constexpr int SMEM_BYTES = OFF_MISC + 128 + 1024;
+  // misc: abort flag, bad | scan [5] | b0 | base of b0 | per-warp ok [4]
+  static constexpr int SMEM_BYTES = OFF_MISC + 96 + 1024;
   static constexpr int THREADS = 32 * (NW + 1);
-  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+  static constexpr int CTAS = cdec_ctas_per_sm(NB);
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
 };
 
 // First and one-past-last 64-key tile that any query of an entry of length L
@@ -106,16 +114,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// transpose an 8 x 8 matrix of halves held two per lane (row lane / 4)
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(160, 2)
+template <int D, int NB, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                            const CDecParams p) {
-  using C = CDecCfg<D>;
+  using C = CDecCfg<D, NB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -138,6 +152,7 @@ __global__ void __launch_bounds__(160, 2)
     fence_mbar_init();
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end itself
 
   // ---- this CTA's units: every thread sums a run of entries, block scan
   const int per = (p.B + C::THREADS - 1) / C::THREADS;
@@ -270,38 +285,36 @@ __global__ void __launch_bounds__(160, 2)
   // -------------------------------------------------------------- compute
   const int g = lane >> 2, t = lane & 3;
   constexpr int KS = D / 16;      // k-steps of the scores
-  constexpr int ND = D / 8;       // output columns per (g): n-tiles of the second product
-  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC) + warp * 64;
+  constexpr int MT = D / 16;      // 16-dimension tiles of the output
   float* sMl = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* sAcc = reinterpret_cast<float*>(smem + C::OFF_ACC);
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kLazy = 8.f;    // the maxima move when exceeded by more than 2^8
+  const bool windowed = p.window > 0 && p.window < p.Nk;
   int gtile = 0;
   Walk w;
   walk_begin(w);
   for (long long u = u0; u < u1;) {
     const int n = static_cast<int>(min(static_cast<long long>(w.r.t1 - w.tp), u1 - u));
     const int L = w.L;
-    // ---- query rows g and g + 8 of this row block: thread t takes D / 4
-    // contiguous dimensions; scaled by 2^-a to below 2^15
-    uint32_t qa[KS][4];
-    float rowf[2];                 // score factor of the row
-    float slope[2] = {0.f, 0.f};
-    int pos[2];                    // the query's position
-    bool row_ok[2];
+    // ---- query rows 8 nb + g of this row block: thread t takes D / 4
+    // contiguous dimensions; scaled by 2^-a to below 2^15.  The scores come out
+    // with rows 8 nb + 2t, 2t + 1 in this thread: row x = 2 nb + e below.
+    uint32_t qb[NB][KS][2];
+    float rowf[2 * NB], slope[2 * NB];
+    int pos[2 * NB];               // the query's position
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = w.rb * 16 + g + 8 * e;
-      row_ok[e] = r < p.rows;
-      const int qi = row_ok[e] ? r / p.G : 0, h = w.hk * p.G + (row_ok[e] ? r % p.G : 0);
-      pos[e] = L - p.Nq + qi;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = w.rb * C::R + 8 * nb + g;
+      const bool row_ok = r < p.rows;
+      const int qi = row_ok ? r / p.G : 0, h = w.hk * p.G + (row_ok ? r % p.G : 0);
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const __nv_bfloat16*>(p.q) + ((static_cast<size_t>(w.b) * p.Nq + qi) * p.H + h) * D + t * (D / 4));
       uint32_t x[D / 8];
       float a = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 v = row_ok[e] ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = row_ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         x[4 * i] = v.x;
         x[4 * i + 1] = v.y;
         x[4 * i + 2] = v.z;
@@ -314,38 +327,58 @@ __global__ void __launch_bounds__(160, 2)
       // 2^ea: exponent that brings a below 2^15 (0 stays 0; subnormals gain at most 2^120)
       const int ea = a > 0.f ? max(static_cast<int>(__float_as_uint(a) >> 23) - 127 - 14, -120) : 0;
       const float mul = __uint_as_float(static_cast<uint32_t>(127 - ea) << 23);
-      rowf[e] = (CAP ? p.x_mul : p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + ea) << 23);
-      if (BIAS) slope[e] = p.slopes[h] * kLog2e;
+      const float rf = (CAP ? p.x_mul : p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + ea) << 23);
+      const float sl = BIAS ? p.slopes[h] * kLog2e : 0.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {  // k-step s: this thread's dimensions 4s .. 4s + 3
-        qa[s][e] = pack_h2(bf16lo_to_f32(x[2 * s]) * mul, bf16hi_to_f32(x[2 * s]) * mul);
-        qa[s][2 + e] = pack_h2(bf16lo_to_f32(x[2 * s + 1]) * mul, bf16hi_to_f32(x[2 * s + 1]) * mul);
+        qb[nb][s][0] = pack_h2(bf16lo_to_f32(x[2 * s]) * mul, bf16hi_to_f32(x[2 * s]) * mul);
+        qb[nb][s][1] = pack_h2(bf16lo_to_f32(x[2 * s + 1]) * mul, bf16hi_to_f32(x[2 * s + 1]) * mul);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int from = (2 * t + e) * 4;  // a lane that loaded row 2t + e
+        rowf[2 * nb + e] = __shfl_sync(0xffffffffu, rf, from);
+        slope[2 * nb + e] = BIAS ? __shfl_sync(0xffffffffu, sl, from) : 0.f;
+        pos[2 * nb + e] = L - p.Nq + __shfl_sync(0xffffffffu, qi, from);
       }
     }
-    float m[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[ND][4];
+    float m[2 * NB], mo[2 * NB], l[2 * NB];
 #pragma unroll
-    for (int c = 0; c < ND; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+    for (int x = 0; x < 2 * NB; ++x) {
+      m[x] = mo[x] = -INFINITY;
+      l[x] = 0.f;
+    }
+    float acc[MT][NB][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[i][nb][0] = acc[i][nb][1] = acc[i][nb][2] = acc[i][nb][3] = 0.f;
 
-    // scale bytes of this warp's 16 keys, one lane each (lanes 16-31: values),
-    // fetched one tile ahead
-    const uint8_t* exps = (lane < 16 ? p.kexp : p.vexp) + (static_cast<size_t>(w.b) * p.Hkv + w.hk) * p.Nk;
-    auto fetch_exp = [&](int tile) -> uint32_t {
-      const int key = tile * C::KT + warp * 16 + (lane & 15);
-      return key < L ? exps[key] : 127u;
+    // exponent bytes of this thread's keys g, g + 8 (keys, values), fetched one tile ahead
+    const size_t plane = (static_cast<size_t>(w.b) * p.Hkv + w.hk) * p.Nk;
+    uint32_t ex[4];
+    auto fetch_exp = [&](int tile) {
+      const int key = tile * C::KT + warp * 16 + g;
+      const bool a = key < L, c = key + 8 < L;
+      ex[0] = a ? p.kexp[plane + key] : 127u;
+      ex[1] = c ? p.kexp[plane + key + 8] : 127u;
+      ex[2] = a ? p.vexp[plane + key] : 127u;
+      ex[3] = c ? p.vexp[plane + key + 8] : 127u;
     };
-    uint32_t ex = fetch_exp(w.tp);
-    // keys that some query of the entry sees
-    const int key_lo = p.window > 0 && p.window < p.Nk ? L - p.Nq - p.window + 1 : 0;
+    fetch_exp(w.tp);
+    // keys that some query of the entry sees, and keys that all of them see
+    const int key_lo = windowed ? L - p.Nq - p.window + 1 : 0;
+    const int full_lo = windowed ? L - p.window : 0;
+    const int full_hi = min(p.causal ? L - p.Nq + 1 : L, windowed ? L - p.Nq + p.window : L);
     bool ok = true;
     for (int it = 0; it < n; ++it, ++gtile) {
       const int st = gtile % C::NSTAGE;
       const int k0 = (w.tp + it) * C::KT + warp * 16;  // this warp's first key
-      __syncwarp();
-      // keys: the scale itself; values: its exponent
-      sSc[lane] = lane < 16 ? e8m0_value(ex) : (ex == 255u ? __uint_as_float(0x7fffffffu) : static_cast<float>(ex) - 127.f);
-      if (it + 1 < n) ex = fetch_exp(w.tp + it + 1);
-      __syncwarp();
+      // score factor and value exponent of keys g and g + 8
+      const float ks[2] = {e8m0_value(ex[0]), e8m0_value(ex[1])};
+      const float ev[2] = {ex[2] == 255u ? __uint_as_float(0x7fffffffu) : static_cast<float>(ex[2]) - 127.f,
+                           ex[3] == 255u ? __uint_as_float(0x7fffffffu) : static_cast<float>(ex[3]) - 127.f};
+      if (it + 1 < n) fetch_exp(w.tp + it + 1);
       ok = mbar_wait(bar(C::BAR_FULL + st), (gtile / C::NSTAGE) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -354,92 +387,23 @@ __global__ void __launch_bounds__(160, 2)
       const uint8_t* pK = smem + C::OFF_KV + st * 2 * C::TILE + warp * 16 * D;
       const uint8_t* pV = pK + C::TILE;
       if (k0 < L) {  // warp-uniform
-        // ---- scores: two n-tiles of 8 keys
-        float sc[2][4];
+        // ---- scores: keys g and g + 8
+        uint32_t kw[2][KS];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
-          const int r = 8 * x + g;  // key row within the warp's 16
-          uint32_t kw[KS];
+          const int r = 8 * x + g;
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) {
             // 16-byte chunk (D / 64) t + i of the row, swizzled as TMA wrote it
             const int ch = (D == 128) ? ((2 * t + i) ^ (r & 7)) : (t ^ ((r >> 1) & 3));
             const uint4 v = *reinterpret_cast<const uint4*>(pK + r * D + ch * 16);
-            kw[4 * i] = v.x;
-            kw[4 * i + 1] = v.y;
-            kw[4 * i + 2] = v.z;
-            kw[4 * i + 3] = v.w;
-          }
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-            mma_f16(sc[x], qa[s][0], qa[s][1], qa[s][2], qa[s][3], e4m3x2_to_h2(kw[s]), e4m3x2_to_h2(kw[s] >> 16));
-        }
-        // ---- z in base 2, mask, maxima.  Element c: row g + 8 (c >> 1), key
-        // 8x + 2t + (c & 1)
-        float mx[2] = {-INFINITY, -INFINITY}, mxo[2] = {-INFINITY, -INFINITY};
-        float so[2][4];  // z + ev: exponent of the weight; a select, so that an
-                         // unseen key's scale (NaN perhaps) stays out
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float2 ks = *reinterpret_cast<const float2*>(sSc + 8 * x + 2 * t);
-          const float2 vs = *reinterpret_cast<const float2*>(sSc + 16 + 8 * x + 2 * t);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int e = c >> 1;
-            const int key = k0 + 8 * x + 2 * t + (c & 1);
-            float z = sc[x][c] * rowf[e] * ((c & 1) ? ks.y : ks.x);
-            if (CAP) z = p.cap_log2 * tanh_any(z);
-            const int away = pos[e] - key;
-            if (BIAS) z = fmaf(-slope[e], fabsf(static_cast<float>(away)), z);
-            const bool see = key < L && (!p.causal || away >= 0) &&
-                             (p.window <= 0 || (away < p.window && -away < p.window));
-            sc[x][c] = see ? z : -INFINITY;
-            so[x][c] = see ? z + ((c & 1) ? vs.y : vs.x) : -INFINITY;
-            mx[e] = fmaxf(mx[e], sc[x][c]);
-            mxo[e] = fmaxf(mxo[e], so[x][c]);
+            kw[x][4 * i] = v.x;
+            kw[x][4 * i + 1] = v.y;
+            kw[x][4 * i + 2] = v.z;
+            kw[x][4 * i + 3] = v.w;
           }
         }
-        bool move = false;
-        float al[2], alo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-          mxo[e] = fmaxf(mxo[e], __shfl_xor_sync(0xffffffffu, mxo[e], 1));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-          mxo[e] = fmaxf(mxo[e], __shfl_xor_sync(0xffffffffu, mxo[e], 2));
-          al[e] = alo[e] = 1.f;
-          if (mx[e] > m[e] + kLazy || (m[e] == -INFINITY && mx[e] > -INFINITY)) {
-            al[e] = ex2(m[e] - mx[e]);
-            m[e] = mx[e];
-          }
-          if (mxo[e] > mo[e] + kLazy || (mo[e] == -INFINITY && mxo[e] > -INFINITY)) {
-            alo[e] = ex2(mo[e] - mxo[e]);
-            mo[e] = mxo[e];
-            move = true;
-          }
-          l[e] *= al[e];
-        }
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int c = 0; c < ND; ++c) {
-            acc[c][0] *= alo[0];
-            acc[c][1] *= alo[0];
-            acc[c][2] *= alo[1];
-            acc[c][3] *= alo[1];
-          }
-        }
-        // ---- weights: A operand of the second product
-        uint32_t wa[4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float nm = m[e] == -INFINITY ? 0.f : -m[e], nmo = mo[e] == -INFINITY ? 0.f : -mo[e];
-            l[e] += ex2(sc[x][2 * e] + nm) + ex2(sc[x][2 * e + 1] + nm);
-            wa[2 * x + e] = pack_h2(ex2(so[x][2 * e] + nmo), ex2(so[x][2 * e + 1] + nmo));
-          }
-        // ---- output: keys 2t, 2t+1 (first half of k) and 2t+8, 2t+9
+        // the values' loads, early: keys 2t, 2t+1 (first half of k) and 2t+8, 2t+9
         uint32_t vw[4][D / 32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -456,6 +420,85 @@ __global__ void __launch_bounds__(160, 2)
             vw[i][1] = v.y;
           }
         }
+        float sc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint32_t a0 = e4m3x2_to_h2(kw[0][s]), a1 = e4m3x2_to_h2(kw[1][s]), a2 = e4m3x2_to_h2(kw[0][s] >> 16),
+                         a3 = e4m3x2_to_h2(kw[1][s] >> 16);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16(sc[nb], a0, a1, a2, a3, qb[nb][s][0], qb[nb][s][1]);
+        }
+        // ---- z in base 2 and exponents of the weights, zo = z + ev.  Element c:
+        // key g + 8 (c >> 1), row x = 2 nb + (c & 1).  A key that a row does not
+        // see is a select, so that its scale (NaN perhaps) stays out.
+        const bool all_see = k0 >= full_lo && k0 + 16 <= full_hi;  // warp-uniform
+        float so[NB][4];
+        bool over = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int x = 2 * nb + (c & 1), key = k0 + g + 8 * (c >> 1);
+            float z = sc[nb][c] * (rowf[x] * ks[c >> 1]);
+            if (CAP) z = p.cap_log2 * tanh_any(z);
+            if (BIAS) z = fmaf(-slope[x], fabsf(static_cast<float>(pos[x] - key)), z);
+            float zo = z + ev[c >> 1];
+            if (!all_see) {
+              const int away = pos[x] - key;
+              const bool see = key < L && (!p.causal || away >= 0) &&
+                               (p.window <= 0 || (away < p.window && -away < p.window));
+              z = see ? z : -INFINITY;
+              zo = see ? zo : -INFINITY;
+            }
+            sc[nb][c] = z;
+            so[nb][c] = zo;
+            over |= z > m[x] + kLazy || zo > mo[x] + kLazy;
+          }
+        if (__any_sync(0xffffffffu, over)) {  // some maximum moves: reduce it over the keys' lanes
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int x = 2 * nb + e;
+              float a = fmaxf(sc[nb][e], sc[nb][2 + e]), b = fmaxf(so[nb][e], so[nb][2 + e]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+              }
+              if (a > m[x]) {
+                l[x] *= ex2(m[x] - a);
+                m[x] = a;
+              }
+              if (b > mo[x]) {
+                const float f = ex2(mo[x] - b);
+                mo[x] = b;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  acc[i][nb][e] *= f;
+                  acc[i][nb][2 + e] *= f;
+                }
+              }
+            }
+        }
+        // ---- weights, from (key, row pair) to (row, key pair) lanes
+        uint32_t wb[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float nm[2], nmo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int x = 2 * nb + e;
+            nm[e] = m[x] == -INFINITY ? 0.f : m[x];
+            nmo[e] = mo[x] == -INFINITY ? 0.f : mo[x];
+            l[x] += ex2(sc[nb][e] - nm[e]) + ex2(sc[nb][2 + e] - nm[e]);
+          }
+          wb[nb][0] = movmatrix_trans(pack_h2(ex2(so[nb][0] - nmo[0]), ex2(so[nb][1] - nmo[1])));
+          wb[nb][1] = movmatrix_trans(pack_h2(ex2(so[nb][2] - nmo[0]), ex2(so[nb][3] - nmo[1])));
+        }
+        // ---- output
         if (k0 + 16 > L || k0 < key_lo) {  // rows no query sees may hold NaN codes: 0 x NaN
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -466,14 +509,19 @@ __global__ void __launch_bounds__(160, 2)
           }
         }
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {  // four output columns at a time
-          // bytes (key, key + 1) of columns 4c .. 4c + 3
+        for (int c = 0; c < D / 32; ++c) {  // four dimensions, two output tiles at a time
+          // bytes (key, key + 1) of dimensions 4c .. 4c + 3 of the thread's chunk
           const uint32_t a01 = __byte_perm(vw[0][c], vw[1][c], 0x5140), a23 = __byte_perm(vw[0][c], vw[1][c], 0x7362);
           const uint32_t b01 = __byte_perm(vw[2][c], vw[3][c], 0x5140), b23 = __byte_perm(vw[2][c], vw[3][c], 0x7362);
-          mma_f16(acc[4 * c + 0], wa[0], wa[1], wa[2], wa[3], e4m3x2_to_h2(a01), e4m3x2_to_h2(b01));
-          mma_f16(acc[4 * c + 1], wa[0], wa[1], wa[2], wa[3], e4m3x2_to_h2(a01 >> 16), e4m3x2_to_h2(b01 >> 16));
-          mma_f16(acc[4 * c + 2], wa[0], wa[1], wa[2], wa[3], e4m3x2_to_h2(a23), e4m3x2_to_h2(b23));
-          mma_f16(acc[4 * c + 3], wa[0], wa[1], wa[2], wa[3], e4m3x2_to_h2(a23 >> 16), e4m3x2_to_h2(b23 >> 16));
+          const uint32_t h0 = e4m3x2_to_h2(a01), h1 = e4m3x2_to_h2(a01 >> 16), h2 = e4m3x2_to_h2(b01),
+                         h3 = e4m3x2_to_h2(b01 >> 16);
+          const uint32_t i0 = e4m3x2_to_h2(a23), i1 = e4m3x2_to_h2(a23 >> 16), i2 = e4m3x2_to_h2(b23),
+                         i3 = e4m3x2_to_h2(b23 >> 16);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_f16(acc[2 * c][nb], h0, h1, h2, h3, wb[nb][0], wb[nb][1]);
+            mma_f16(acc[2 * c + 1][nb], i0, i1, i2, i3, wb[nb][0], wb[nb][1]);
+          }
         }
       }
       mbar_arrive(bar(C::BAR_EMPTY + st));
@@ -481,13 +529,14 @@ __global__ void __launch_bounds__(160, 2)
     // ---- join the four warps: rows of the block in passes of four
     if (lane == 0) s_ok[warp] = ok;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      if (t == 0) {
-        sMl[(0 * C::NW + warp) * 16 + g + 8 * e] = m[e];
-        sMl[(1 * C::NW + warp) * 16 + g + 8 * e] = mo[e];
-        sMl[(2 * C::NW + warp) * 16 + g + 8 * e] = l[e];
+    for (int x = 0; x < 2 * NB; ++x) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], off);
+      if (g == 0) {
+        const int row = 8 * (x >> 1) + 2 * t + (x & 1);
+        sMl[(0 * C::NW + warp) * C::R + row] = m[x];
+        sMl[(1 * C::NW + warp) * C::R + row] = mo[x];
+        sMl[(2 * C::NW + warp) * C::R + row] = l[x];
       }
     }
     named_bar_sync(1, C::NW * 32);
@@ -496,69 +545,69 @@ __global__ void __launch_bounds__(160, 2)
     if (!(s_ok[0] && s_ok[1] && s_ok[2] && s_ok[3])) return;
     const bool whole = w.tp == w.r.t0 && n == w.r.t1 - w.r.t0;  // the piece is the whole segment
     const int slot = (u == u0) ? 0 : 1;
-    const int nrows = min(16, p.rows - w.rb * 16);
-    float f[2];  // this warp's output factor per row: 2^(mo_w - mo), 0 when it saw nothing
+    const int nrows = min(C::R, p.rows - w.rb * C::R);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float M = -INFINITY;
-      for (int x = 0; x < C::NW; ++x) M = fmaxf(M, sMl[(C::NW + x) * 16 + g + 8 * e]);
-      f[e] = mo[e] == -INFINITY ? 0.f : ex2(mo[e] - M);
-    }
-    for (int r0 = 0; r0 < nrows; r0 += 4) {
-      // rows r0 .. r0 + 3: lanes g = r0 % 8 .. + 3, half e = r0 / 8
-      const int e = r0 >> 3;
-      if ((g & 4) == (r0 & 4)) {
-        float* dst = sAcc + (warp * 4 + (g & 3)) * C::ACC_LD + t * (D / 4);
-        const float fe = e ? f[1] : f[0];
+    for (int x4 = 0; x4 < 2 * NB; ++x4) {  // rows 4 x4 .. 4 x4 + 3: lanes t = 2 (x4 & 1), + 1
+      const int r0 = 4 * x4, nb = x4 >> 1;
+      if (r0 < nrows) {
+        if ((t >> 1) == (x4 & 1)) {
 #pragma unroll
-        for (int c = 0; c < ND; ++c) {
-          // column 2t, 2t + 1 of n-tile c: dimensions (2t) ND + c and (2t + 1) ND + c
-          dst[c] = (e ? acc[c][2] : acc[c][0]) * fe;
-          dst[ND + c] = (e ? acc[c][3] : acc[c][1]) * fe;
-        }
-      }
-      named_bar_sync(1, C::NW * 32);
-      const int rr = threadIdx.x >> 5;  // warp = row of the pass
-      const int row = r0 + rr;
-      if (row < nrows) {
-        float M = -INFINITY, MO = -INFINITY, lsum = 0.f;
+          for (int e = 0; e < 2; ++e) {
+            const int x = 2 * nb + e, row = 8 * nb + 2 * t + e;
+            float M = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < C::NW; ++x) {
-          M = fmaxf(M, sMl[x * 16 + row]);
-          MO = fmaxf(MO, sMl[(C::NW + x) * 16 + row]);
-        }
+            for (int y = 0; y < C::NW; ++y) M = fmaxf(M, sMl[(C::NW + y) * C::R + row]);
+            // this warp's output factor: 2^(mo_w - mo), 0 when it saw nothing
+            const float f = mo[x] == -INFINITY ? 0.f : ex2(mo[x] - M);
+            float* dst = sAcc + (warp * 4 + (row & 3)) * C::ACC_LD + g * (D / 8);
 #pragma unroll
-        for (int x = 0; x < C::NW; ++x) {
-          const float mw = sMl[x * 16 + row];
-          if (mw != -INFINITY) lsum += sMl[(2 * C::NW + x) * 16 + row] * ex2(mw - M);
-          else if (sMl[(2 * C::NW + x) * 16 + row] != 0.f) lsum = sMl[(2 * C::NW + x) * 16 + row];  // NaN scores
-        }
-        const float inv = lsum == 0.f ? 0.f : ex2(MO - M) / lsum;
-        const float lse = lsum == 0.f ? -INFINITY : (M + lg2(lsum)) * kLn2;
-        const int r = w.rb * 16 + row, qi = r / p.G, h = w.hk * p.G + r % p.G;
-        const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + slot) * 16 + row;
-        for (int c = lane * 2; c < D; c += 64) {
-          float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-          for (int x = 0; x < C::NW; ++x) {
-            const float2 v = *reinterpret_cast<const float2*>(sAcc + (x * 4 + rr) * C::ACC_LD + c);
-            a0 += v.x;
-            a1 += v.y;
+            for (int i = 0; i < MT; ++i)
+              *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nb][e] * f, acc[i][nb][2 + e] * f);
           }
-          a0 *= inv;
-          a1 *= inv;
-          if (whole)
-            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                         ((static_cast<size_t>(w.b) * p.Nq + qi) * p.H + h) * D + c) = pack_bf16x2(a0, a1);
-          else
-            *reinterpret_cast<float2*>(p.rec_o + rec * D + c) = make_float2(a0, a1);
         }
-        if (lane == 0) {
-          if (whole) p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.Nq + qi] = lse;
-          else p.rec_lse[rec] = lse;
+        named_bar_sync(1, C::NW * 32);
+        const int row = r0 + warp;  // warp = row of the pass
+        if (row < nrows) {
+          float M = -INFINITY, MO = -INFINITY, lsum = 0.f;
+#pragma unroll
+          for (int y = 0; y < C::NW; ++y) {
+            M = fmaxf(M, sMl[y * C::R + row]);
+            MO = fmaxf(MO, sMl[(C::NW + y) * C::R + row]);
+          }
+#pragma unroll
+          for (int y = 0; y < C::NW; ++y) {
+            const float mw = sMl[y * C::R + row], lw = sMl[(2 * C::NW + y) * C::R + row];
+            // a warp without a maximum has seen nothing (l = 0) or NaN only (l = NaN)
+            lsum += mw == -INFINITY ? lw : lw * ex2(mw - M);
+          }
+          const float inv = lsum == 0.f ? 0.f : ex2(MO - M) / lsum;
+          const float lse = lsum == 0.f ? -INFINITY : (M + lg2(lsum)) * kLn2;
+          const int r = w.rb * C::R + row, qi = r / p.G, h = w.hk * p.G + r % p.G;
+          const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + slot) * C::R + row;
+          for (int c = lane * 2; c < D; c += 64) {
+            float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+            for (int y = 0; y < C::NW; ++y) {
+              const float2 v = *reinterpret_cast<const float2*>(sAcc + (y * 4 + warp) * C::ACC_LD + c);
+              a0 += v.x;
+              a1 += v.y;
+            }
+            a0 *= inv;
+            a1 *= inv;
+            if (whole)
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
+                                           ((static_cast<size_t>(w.b) * p.Nq + qi) * p.H + h) * D + c) =
+                  pack_bf16x2(a0, a1);
+            else
+              *reinterpret_cast<float2*>(p.rec_o + rec * D + c) = make_float2(a0, a1);
+          }
+          if (lane == 0) {
+            if (whole) p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.Nq + qi] = lse;
+            else p.rec_lse[rec] = lse;
+          }
         }
+        named_bar_sync(1, C::NW * 32);
       }
-      named_bar_sync(1, C::NW * 32);
     }
     u += n;
     w.tp += n;
@@ -566,14 +615,18 @@ __global__ void __launch_bounds__(160, 2)
   }
 }
 
-// One warp per output row (batch entry, head, query): rows of entries whose
-// queries see no tile get O = 0, LSE = -inf; rows of segments shared by
-// several CTAs are combined from their records; the rest is written already.
+// One block per output row (batch entry, head, query): rows of entries whose
+// queries see no tile get O = 0, LSE = -inf; rows of segments shared by several
+// CTAs are combined from their records (the four warps take every fourth
+// record, four loads in flight each); the rest is written already.
 __global__ void __launch_bounds__(128) fa_cache_decode_merge_kernel(const CDecParams p, int D) {
+  __shared__ float s_w[kCacheDecodeGridMax];
+  __shared__ float s_red[4];
+  __shared__ float s_acc[3][128];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the stream kernel has ended and its writes are visible
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-  const long long nrows = static_cast<long long>(p.B) * p.H * p.Nq;
-  if (row >= nrows || *p.bad) return;
+  if (*p.bad) return;
+  const long long row = blockIdx.x;
   const int qi = static_cast<int>(row % p.Nq);
   const long long bh = row / p.Nq;
   const int b = static_cast<int>(bh / p.H), h = static_cast<int>(bh % p.H);
@@ -582,47 +635,68 @@ __global__ void __launch_bounds__(128) fa_cache_decode_merge_kernel(const CDecPa
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<size_t>(b) * p.Nq + qi) * p.H + h) * D;
   float* lse = p.lse + bh * p.Nq + qi;
   if (T == 0) {
-    for (int c = lane; c < D; c += 32) out[c] = __float2bfloat16(0.f);
-    if (lane == 0) *lse = -INFINITY;
+    if (threadIdx.x < D) out[threadIdx.x] = __float2bfloat16(0.f);
+    if (threadIdx.x == 0) *lse = -INFINITY;
     return;
   }
   const long long U = p.prefix[p.B];
   const long long chunk = (U + p.grid - 1) / p.grid;
   const int r = qi * p.G + h % p.G;  // row of its key head
-  const long long s0 = p.prefix[b] + (static_cast<long long>(h / p.G) * p.nrb + (r >> 4)) * T, s1 = s0 + T;
+  const long long s0 = p.prefix[b] + (static_cast<long long>(h / p.G) * p.nrb + r / p.rpb) * T, s1 = s0 + T;
   const int g0 = static_cast<int>(s0 / chunk), g1 = static_cast<int>((s1 - 1) / chunk);
   if (g0 == g1) return;
   const int n = g1 - g0 + 1;
   // CTA g0's piece is its last one (slot 1) unless its chunk starts with the
   // segment; every later CTA's piece is its first one (slot 0)
   const int slot0 = static_cast<long long>(g0) * chunk < s0 ? 1 : 0;
-  auto rec = [&](int k) -> size_t { return (static_cast<size_t>(g0 + k) * 2 + (k == 0 ? slot0 : 0)) * 16 + (r & 15); };
+  auto rec = [&](int k) -> size_t {
+    return (static_cast<size_t>(g0 + k) * 2 + (k == 0 ? slot0 : 0)) * p.rpb + r % p.rpb;
+  };
+  constexpr float kLog2ef = 1.4426950408889634f;
   float mx = -INFINITY;
-  bool nan = false;
-  for (int k = lane; k < n; k += 32) {
+  for (int k = threadIdx.x; k < n; k += 128) {
     const float x = p.rec_lse[rec(k)];
-    nan |= x != x;
+    s_w[k] = x;
     mx = fmaxf(mx, x);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  nan = __any_sync(0xffffffffu, nan);
-  constexpr float kLog2ef = 1.4426950408889634f;
+  if (lane == 0) s_red[warp] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  const float ref = mx == -INFINITY ? 0.f : mx;  // no record with a weight: all 0 (or NaN)
   float den = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < n; ++k) {
-    const float lr = p.rec_lse[rec(k)];
-    if (lr == -INFINITY) continue;
-    const float wk = ex2((lr - mx) * kLog2ef);
+  const int cols = D / 32;
+#pragma unroll 4
+  for (int k = warp; k < n; k += 4) {
+    const float wk = ex2((s_w[k] - ref) * kLog2ef);
+    const float* o = p.rec_o + rec(k) * D + lane * cols;
     den += wk;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (lane + 32 * c < D) acc[c] = fmaf(wk, p.rec_o[rec(k) * D + lane + 32 * c], acc[c]);
+    if (cols == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(o);
+      acc[0] = fmaf(wk, v.x, acc[0]);
+      acc[1] = fmaf(wk, v.y, acc[1]);
+      acc[2] = fmaf(wk, v.z, acc[2]);
+      acc[3] = fmaf(wk, v.w, acc[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(o);
+      acc[0] = fmaf(wk, v.x, acc[0]);
+      acc[1] = fmaf(wk, v.y, acc[1]);
+    }
   }
+  __syncthreads();  // s_red has been read
+  if (lane == 0) s_red[warp] = den;
+  if (warp > 0)
+    for (int c = 0; c < cols; ++c) s_acc[warp - 1][lane * cols + c] = acc[c];
+  __syncthreads();
+  if (warp > 0) return;
+  den = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
   const float inv = den == 0.f ? 0.f : 1.f / den;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < D) out[lane + 32 * c] = __float2bfloat16(acc[c] * inv);
-  if (lane == 0) *lse = nan ? __uint_as_float(0x7fffffffu) : (den == 0.f ? -INFINITY : mx + lg2(den) * kLn2);
+  for (int c = 0; c < cols; ++c) {
+    const int x = lane * cols + c;
+    out[x] = __float2bfloat16((acc[c] + s_acc[0][x] + s_acc[1][x] + s_acc[2][x]) * inv);
+  }
+  if (lane == 0) *lse = den == 0.f ? -INFINITY : ref + lg2(den) * kLn2;
 }
 
 }  // namespace fa
