@@ -566,9 +566,11 @@ fa_status cache_check(int B, int Nk, int Hkv, int d) {
 struct CacheDecodeWs {
   size_t prefix, bad, rec_o, rec_lse, total;
 };
-CacheDecodeWs cache_decode_ws(int B, int d) {
+CacheDecodeWs cache_decode_ws(int B, int Hkv, int d) {
   CacheDecodeWs w;
-  const size_t recs = static_cast<size_t>(fa::kCacheDecodeGridMax) * 2 * 16;
+  // CTAs of the stream kernel: at most one wave, or one group where Hkv is more
+  const size_t ctas = Hkv > fa::kCacheDecodeGroupsMax ? Hkv : fa::kCacheDecodeGroupsMax;
+  const size_t recs = ctas * 2 * 16;
   w.prefix = 0;
   w.bad = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
   w.rec_o = w.bad + 256;
@@ -589,9 +591,12 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   if (st != FA_OK) return st;
   p.rpb = 8 * NB;
   p.nrb = (p.rows + p.rpb - 1) / p.rpb;
-  p.grid = fa::cdec_ctas_per_sm(NB) * 148;
+  const int wave = fa::cdec_ctas_per_sm(NB) * 148;
+  p.groups = p.Hkv > wave ? 1 : wave / p.Hkv;
+  // a CTA's share of the 64-key tiles is counted in 32 bits
+  if (static_cast<int64_t>(p.B) * p.nrb * ((p.Nk + 63) / 64) / p.groups >= 0x7fffffff) return FA_ERR_INVALID_ARG;
   mark_launch(s);
-  kern<<<static_cast<unsigned>(p.grid), fa::CDecCfg<D, NB>::THREADS, smem, s>>>(mk, mv, p);
+  kern<<<static_cast<unsigned>(p.groups) * p.Hkv, fa::CDecCfg<D, NB>::THREADS, smem, s>>>(mk, mv, p);
   if ((st = launch_status(s)) != FA_OK) return st;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -975,7 +980,7 @@ fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens
 size_t fa_cache_decode_workspace_size(int B, int Nq, int Nk, int H, int Hkv, int d) {
   if (B < 1 || B > 65535 || Nq < 1 || Nq > 16 || Nk < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128))
     return 0;
-  return cache_decode_ws(B, d).total;
+  return cache_decode_ws(B, Hkv, d).total;
 }
 
 fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
@@ -999,7 +1004,7 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
   if (Nk > (1 << 30) || static_cast<int64_t>(B) * Nq * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * Nq * H > 0x7fffffff || static_cast<int64_t>(H) * Nq > 0x7fffffff)
     return FA_ERR_INVALID_ARG;
-  const CacheDecodeWs wl = cache_decode_ws(B, d);
+  const CacheDecodeWs wl = cache_decode_ws(B, Hkv, d);
   if (!workspace || ws_bytes < wl.total) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_INVALID_ARG;
   int dev;

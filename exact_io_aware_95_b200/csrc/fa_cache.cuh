@@ -32,6 +32,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+// the four codes of a word -> halves (codes 0, 1) and (codes 2, 3); the 16-bit
+// halves of the word are named, not shifted out
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t& h01, uint32_t& h23) {
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(h01), "=r"(h23)
+      : "r"(w));
+}
 // two floats -> two e4m3 codes, `lo` in the low byte; saturating, NaN stays NaN
 __device__ __forceinline__ uint32_t pack_e4m3x2_sat(float lo, float hi) {
   unsigned short r;

@@ -37,10 +37,15 @@
 //   - Each of the four compute warps owns 16 keys of a 64-key tile with its own
 //     running maxima, sums and output: no block-wide step per tile.  They are
 //     joined in shared memory at the end of a segment piece.
-// Work split: as fa_decode.cuh, stream-K over (batch entry, key head, row
-// block, 64-key tile) units in equal contiguous chunks, partial records of
-// shared segments merged through their logsumexps by a second kernel.  Each CTA
-// finds its chunk by scanning the lengths itself: no prefix launch.
+// Work split: stream-K as in fa_decode.cuh, but over (batch entry, row block,
+// 64-key tile) units without the head: the CTAs form groups of Hkv, a group
+// takes a contiguous chunk of the units, and each of its CTAs does them for one
+// key head.  A token's heads are neighbours in memory and a head's row is only
+// d bytes, so a group's CTAs, walking the same tokens side by side, read whole
+// DRAM pages between them; one head after the other, the same copies without
+// any arithmetic streamed at 4.2 TB/s.  Partial records of shared segments are
+// merged through their logsumexps by a second kernel.  Each CTA finds its chunk
+// by scanning the lengths itself: no prefix launch.
 #pragma once
 #include "fa_cache.cuh"
 #include "fa_mod_fwd.cuh"
@@ -50,7 +55,7 @@ namespace fa {
 // Stream CTAs: one wave.  NB = 1 fits three CTAs of 128 registers a thread on
 // an SM, NB = 2 two of 168.
 __host__ __device__ constexpr int cdec_ctas_per_sm(int NB) { return NB == 1 ? 3 : 2; }
-constexpr int kCacheDecodeGridMax = 3 * 148;
+constexpr int kCacheDecodeGroupsMax = 3 * 148;
 
 struct CDecParams {
   const void* q;          // bf16 [B, Nq, H, d]
@@ -62,11 +67,11 @@ struct CDecParams {
   const float* slopes;    // [H] or nullptr
   long long* prefix;      // [B + 1] first unit of each entry, for the merge
   int* bad;
-  float* rec_o;           // [grid][2][8 NB][d]
-  float* rec_lse;         // [grid][2][8 NB]
+  float* rec_o;           // [CTA][2][8 NB][d]
+  float* rec_lse;         // [CTA][2][8 NB]
   int B, Nq, Nk, H, Hkv, G;
   int rows, nrb, rpb;     // G Nq query rows per key head, blocks of rpb = 8 NB
-  int grid, causal, window;
+  int groups, causal, window;  // grid = groups * Hkv CTAs
   float scale_log2;       // scale log2 e          (no cap)
   float x_mul, cap_log2;  // scale / cap, cap log2 e
 };
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     const int L = cdec_len(p, b);
     if (L < 0 || L > p.Nk) return -1;
     const CDecRange r = cdec_range(p, L);
-    return static_cast<long long>(r.t1 - r.t0) * p.Hkv * p.nrb;
+    return static_cast<long long>(r.t1 - r.t0) * p.nrb;
   };
   long long sum = 0;
   bool bad = false;
@@ -185,8 +190,9 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     U += s_scan[w];
   }
   const bool any_bad = *s_bad != 0;
-  const long long chunk = (U + p.grid - 1) / p.grid;
-  const long long u0 = static_cast<long long>(blockIdx.x) * chunk;
+  const long long chunk = (U + p.groups - 1) / p.groups;
+  const int hk = blockIdx.x % p.Hkv;  // this CTA's key head
+  const long long u0 = static_cast<long long>(blockIdx.x / p.Hkv) * chunk;
   const long long u1 = min(U, u0 + chunk);
   if (blockIdx.x == 0) {  // the merge kernel's copy
     long long run = base;
@@ -217,10 +223,10 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   }
   __syncthreads();
 
-  // Walk of the units [u0, u1), the same in both roles: segment (b, hk, rb),
+  // Walk of the units [u0, u1), the same in both roles: segment (b, rb),
   // its tiles [r.t0, r.t1), the current tile tp.
   struct Walk {
-    int b, hk, rb, tp, L;
+    int b, rb, tp, L;
     CDecRange r;
   };
   auto walk_begin = [&](Walk& w) {
@@ -229,22 +235,17 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     w.r = cdec_range(p, w.L);
     const long long rel = u0 - *s_base0;
     const int T = w.r.t1 - w.r.t0;
-    const int seg = static_cast<int>(rel / T);
+    w.rb = static_cast<int>(rel / T);
     w.tp = w.r.t0 + static_cast<int>(rel % T);
-    w.hk = seg / p.nrb;
-    w.rb = seg % p.nrb;
   };
   auto walk_next = [&](Walk& w) {  // after the last tile of a segment, with units left
     if (++w.rb == p.nrb) {
       w.rb = 0;
-      if (++w.hk == p.Hkv) {
-        w.hk = 0;
-        do {
-          ++w.b;
-          w.L = cdec_len(p, w.b);
-          w.r = cdec_range(p, w.L);
-        } while (w.r.t0 >= w.r.t1);
-      }
+      do {
+        ++w.b;
+        w.L = cdec_len(p, w.b);
+        w.r = cdec_range(p, w.L);
+      } while (w.r.t0 >= w.r.t1);
     }
     w.tp = w.r.t0;
   };
@@ -258,7 +259,8 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
       walk_begin(w);
       int issued = 0;
       bool ok = true;
-      for (long long u = u0; ok && u < u1; ++u) {
+      const int total = static_cast<int>(u1 - u0);
+      for (int done = 0; ok && done < total; ++done) {
         const int st = issued % C::NSTAGE;
         if (!(ok = mbar_wait(bar(C::BAR_EMPTY + st), ((issued / C::NSTAGE) & 1) ^ 1u, abort_flag))) break;
         const int row = w.tp * C::KT;
@@ -266,11 +268,11 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
         mbar_arrive_expect_tx(bar(C::BAR_FULL + st), boxes * 2 * 32 * D);
         const uint32_t dst = sbase + C::OFF_KV + st * 2 * C::TILE;
         for (int x = 0; x < boxes; ++x) {
-          tma_load_4d(dst + x * 32 * D, &tmK, bar(C::BAR_FULL + st), 0, w.hk, row + 32 * x, w.b);
-          tma_load_4d(dst + C::TILE + x * 32 * D, &tmV, bar(C::BAR_FULL + st), 0, w.hk, row + 32 * x, w.b);
+          tma_load_4d(dst + x * 32 * D, &tmK, bar(C::BAR_FULL + st), 0, hk, row + 32 * x, w.b);
+          tma_load_4d(dst + C::TILE + x * 32 * D, &tmV, bar(C::BAR_FULL + st), 0, hk, row + 32 * x, w.b);
         }
         ++issued;
-        if (++w.tp == w.r.t1 && u + 1 < u1) walk_next(w);
+        if (++w.tp == w.r.t1 && done + 1 < total) walk_next(w);
       }
       if (*abort_flag) {  // let the copies in flight land before the CTA exits
         for (int n = 0; n < C::NSTAGE && n < issued; ++n) {
@@ -294,8 +296,9 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   int gtile = 0;
   Walk w;
   walk_begin(w);
-  for (long long u = u0; u < u1;) {
-    const int n = static_cast<int>(min(static_cast<long long>(w.r.t1 - w.tp), u1 - u));
+  const int total = static_cast<int>(u1 - u0);  // the host keeps a CTA's share below 2^31
+  for (int done = 0; done < total;) {
+    const int n = min(w.r.t1 - w.tp, total - done);
     const int L = w.L;
     // ---- query rows 8 nb + g of this row block: thread t takes D / 4
     // contiguous dimensions; scaled by 2^-a to below 2^15.  The scores come out
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     for (int nb = 0; nb < NB; ++nb) {
       const int r = w.rb * C::R + 8 * nb + g;
       const bool row_ok = r < p.rows;
-      const int qi = row_ok ? r / p.G : 0, h = w.hk * p.G + (row_ok ? r % p.G : 0);
+      const int qi = row_ok ? r / p.G : 0, h = hk * p.G + (row_ok ? r % p.G : 0);
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const __nv_bfloat16*>(p.q) + ((static_cast<size_t>(w.b) * p.Nq + qi) * p.H + h) * D + t * (D / 4));
       uint32_t x[D / 8];
@@ -355,15 +358,15 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
       for (int nb = 0; nb < NB; ++nb) acc[i][nb][0] = acc[i][nb][1] = acc[i][nb][2] = acc[i][nb][3] = 0.f;
 
     // exponent bytes of this thread's keys g, g + 8 (keys, values), fetched one tile ahead
-    const size_t plane = (static_cast<size_t>(w.b) * p.Hkv + w.hk) * p.Nk;
+    const size_t plane = (static_cast<size_t>(w.b) * p.Hkv + hk) * p.Nk + warp * 16 + g;
+    const uint8_t *ke = p.kexp + plane, *ve = p.vexp + plane;
     uint32_t ex[4];
     auto fetch_exp = [&](int tile) {
-      const int key = tile * C::KT + warp * 16 + g;
-      const bool a = key < L, c = key + 8 < L;
-      ex[0] = a ? p.kexp[plane + key] : 127u;
-      ex[1] = c ? p.kexp[plane + key + 8] : 127u;
-      ex[2] = a ? p.vexp[plane + key] : 127u;
-      ex[3] = c ? p.vexp[plane + key + 8] : 127u;
+      const int k = tile * C::KT, left = L - warp * 16 - g - k;
+      ex[0] = left > 0 ? ke[k] : 127u;
+      ex[1] = left > 8 ? ke[k + 8] : 127u;
+      ex[2] = left > 0 ? ve[k] : 127u;
+      ex[3] = left > 8 ? ve[k + 8] : 127u;
     };
     fetch_exp(w.tp);
     // keys that some query of the entry sees, and keys that all of them see
@@ -403,7 +406,18 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
             kw[x][4 * i + 3] = v.w;
           }
         }
-        // the values' loads, early: keys 2t, 2t+1 (first half of k) and 2t+8, 2t+9
+        float sc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_h2(kw[0][s], a0, a2);
+          e4m3x4_to_h2(kw[1][s], a1, a3);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16(sc[nb], a0, a1, a2, a3, qb[nb][s][0], qb[nb][s][1]);
+        }
+        // the values' loads, ahead of the softmax arithmetic: keys 2t, 2t+1 (first half of k) and 2t+8, 2t+9
         uint32_t vw[4][D / 32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -419,16 +433,6 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
             vw[i][0] = v.x;
             vw[i][1] = v.y;
           }
-        }
-        float sc[NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const uint32_t a0 = e4m3x2_to_h2(kw[0][s]), a1 = e4m3x2_to_h2(kw[1][s]), a2 = e4m3x2_to_h2(kw[0][s] >> 16),
-                         a3 = e4m3x2_to_h2(kw[1][s] >> 16);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16(sc[nb], a0, a1, a2, a3, qb[nb][s][0], qb[nb][s][1]);
         }
         // ---- z in base 2 and exponents of the weights, zo = z + ev.  Element c:
         // key g + 8 (c >> 1), row x = 2 nb + (c & 1).  A key that a row does not
@@ -513,10 +517,11 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           // bytes (key, key + 1) of dimensions 4c .. 4c + 3 of the thread's chunk
           const uint32_t a01 = __byte_perm(vw[0][c], vw[1][c], 0x5140), a23 = __byte_perm(vw[0][c], vw[1][c], 0x7362);
           const uint32_t b01 = __byte_perm(vw[2][c], vw[3][c], 0x5140), b23 = __byte_perm(vw[2][c], vw[3][c], 0x7362);
-          const uint32_t h0 = e4m3x2_to_h2(a01), h1 = e4m3x2_to_h2(a01 >> 16), h2 = e4m3x2_to_h2(b01),
-                         h3 = e4m3x2_to_h2(b01 >> 16);
-          const uint32_t i0 = e4m3x2_to_h2(a23), i1 = e4m3x2_to_h2(a23 >> 16), i2 = e4m3x2_to_h2(b23),
-                         i3 = e4m3x2_to_h2(b23 >> 16);
+          uint32_t h0, h1, h2, h3, i0, i1, i2, i3;
+          e4m3x4_to_h2(a01, h0, h1);
+          e4m3x4_to_h2(b01, h2, h3);
+          e4m3x4_to_h2(a23, i0, i1);
+          e4m3x4_to_h2(b23, i2, i3);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             mma_f16(acc[2 * c][nb], h0, h1, h2, h3, wb[nb][0], wb[nb][1]);
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     // (every warp reads the same four flags, so all of them leave)
     if (!(s_ok[0] && s_ok[1] && s_ok[2] && s_ok[3])) return;
     const bool whole = w.tp == w.r.t0 && n == w.r.t1 - w.r.t0;  // the piece is the whole segment
-    const int slot = (u == u0) ? 0 : 1;
+    const int slot = done == 0 ? 0 : 1;
     const int nrows = min(C::R, p.rows - w.rb * C::R);
 #pragma unroll
     for (int x4 = 0; x4 < 2 * NB; ++x4) {  // rows 4 x4 .. 4 x4 + 3: lanes t = 2 (x4 & 1), + 1
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           }
           const float inv = lsum == 0.f ? 0.f : ex2(MO - M) / lsum;
           const float lse = lsum == 0.f ? -INFINITY : (M + lg2(lsum)) * kLn2;
-          const int r = w.rb * C::R + row, qi = r / p.G, h = w.hk * p.G + r % p.G;
+          const int r = w.rb * C::R + row, qi = r / p.G, h = hk * p.G + r % p.G;
           const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + slot) * C::R + row;
           for (int c = lane * 2; c < D; c += 64) {
             float a0 = 0.f, a1 = 0.f;
@@ -609,9 +614,9 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
         named_bar_sync(1, C::NW * 32);
       }
     }
-    u += n;
+    done += n;
     w.tp += n;
-    if (w.tp == w.r.t1 && u < u1) walk_next(w);
+    if (w.tp == w.r.t1 && done < total) walk_next(w);
   }
 }
 
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
 // CTAs are combined from their records (the four warps take every fourth
 // record, four loads in flight each); the rest is written already.
 __global__ void __launch_bounds__(128) fa_cache_decode_merge_kernel(const CDecParams p, int D) {
-  __shared__ float s_w[kCacheDecodeGridMax];
+  __shared__ float s_w[kCacheDecodeGroupsMax];
   __shared__ float s_red[4];
   __shared__ float s_acc[3][128];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the stream kernel has ended and its writes are visible
@@ -640,17 +645,18 @@ __global__ void __launch_bounds__(128) fa_cache_decode_merge_kernel(const CDecPa
     return;
   }
   const long long U = p.prefix[p.B];
-  const long long chunk = (U + p.grid - 1) / p.grid;
+  const long long chunk = (U + p.groups - 1) / p.groups;
   const int r = qi * p.G + h % p.G;  // row of its key head
-  const long long s0 = p.prefix[b] + (static_cast<long long>(h / p.G) * p.nrb + r / p.rpb) * T, s1 = s0 + T;
+  const long long s0 = p.prefix[b] + static_cast<long long>(r / p.rpb) * T, s1 = s0 + T;
   const int g0 = static_cast<int>(s0 / chunk), g1 = static_cast<int>((s1 - 1) / chunk);
   if (g0 == g1) return;
   const int n = g1 - g0 + 1;
-  // CTA g0's piece is its last one (slot 1) unless its chunk starts with the
-  // segment; every later CTA's piece is its first one (slot 0)
+  // group g0's piece is its last one (slot 1) unless its chunk starts with the
+  // segment; every later group's piece is its first one (slot 0)
   const int slot0 = static_cast<long long>(g0) * chunk < s0 ? 1 : 0;
   auto rec = [&](int k) -> size_t {
-    return (static_cast<size_t>(g0 + k) * 2 + (k == 0 ? slot0 : 0)) * p.rpb + r % p.rpb;
+    const size_t cta = static_cast<size_t>(g0 + k) * p.Hkv + h / p.G;
+    return (cta * 2 + (k == 0 ? slot0 : 0)) * p.rpb + r % p.rpb;
   };
   constexpr float kLog2ef = 1.4426950408889634f;
   float mx = -INFINITY;
