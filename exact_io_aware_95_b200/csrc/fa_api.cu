@@ -564,16 +564,15 @@ fa_status cache_check(int B, int Nk, int Hkv, int d) {
 }
 
 struct CacheDecodeWs {
-  size_t prefix, bad, rec_o, rec_lse, total;
+  size_t info, rec_o, rec_lse, total;
 };
-CacheDecodeWs cache_decode_ws(int B, int Hkv, int d) {
+CacheDecodeWs cache_decode_ws(int Hkv, int d) {
   CacheDecodeWs w;
   // CTAs of the stream kernel: at most one wave, or one group where Hkv is more
   const size_t ctas = Hkv > fa::kCacheDecodeGroupsMax ? Hkv : fa::kCacheDecodeGroupsMax;
   const size_t recs = ctas * 2 * 16;
-  w.prefix = 0;
-  w.bad = align256((static_cast<size_t>(B) + 1) * sizeof(long long));
-  w.rec_o = w.bad + 256;
+  w.info = 0;
+  w.rec_o = align256(static_cast<size_t>(fa::kCacheDecodeGroupsMax) * sizeof(int4));
   w.rec_lse = w.rec_o + align256(recs * d * sizeof(float));
   w.total = w.rec_lse + align256(recs * sizeof(float));
   return w;
@@ -593,8 +592,9 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   p.nrb = (p.rows + p.rpb - 1) / p.rpb;
   const int wave = fa::cdec_ctas_per_sm(NB) * 148;
   p.groups = p.Hkv > wave ? 1 : wave / p.Hkv;
-  // a CTA's share of the 64-key tiles is counted in 32 bits
-  if (static_cast<int64_t>(p.B) * p.nrb * ((p.Nk + 63) / 64) / p.groups >= 0x7fffffff) return FA_ERR_INVALID_ARG;
+  // an entry's units and a CTA's share of all units are counted in 32 bits
+  const int64_t tiles = static_cast<int64_t>(p.nrb) * ((p.Nk + 63) / 64);
+  if (tiles >= 0x7fffffff || tiles * p.B / p.groups >= 0x7fffffff) return FA_ERR_INVALID_ARG;
   mark_launch(s);
   kern<<<static_cast<unsigned>(p.groups) * p.Hkv, fa::CDecCfg<D, NB>::THREADS, smem, s>>>(mk, mv, p);
   if ((st = launch_status(s)) != FA_OK) return st;
@@ -602,8 +602,8 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * p.Nq));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * p.Hkv, p.rpb / 4);
+  cfg.blockDim = dim3(512);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -980,7 +980,7 @@ fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens
 size_t fa_cache_decode_workspace_size(int B, int Nq, int Nk, int H, int Hkv, int d) {
   if (B < 1 || B > 65535 || Nq < 1 || Nq > 16 || Nk < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128))
     return 0;
-  return cache_decode_ws(B, Hkv, d).total;
+  return cache_decode_ws(Hkv, d).total;
 }
 
 fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
@@ -1002,9 +1002,8 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
   fa_status st = cache_check(B, Nk, Hkv, d);
   if (st != FA_OK) return st;
   if (Nk > (1 << 30) || static_cast<int64_t>(B) * Nq * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(B) * Nq * H > 0x7fffffff || static_cast<int64_t>(H) * Nq > 0x7fffffff)
-    return FA_ERR_INVALID_ARG;
-  const CacheDecodeWs wl = cache_decode_ws(B, Hkv, d);
+  if (static_cast<int64_t>(H) * Nq > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  const CacheDecodeWs wl = cache_decode_ws(Hkv, d);
   if (!workspace || ws_bytes < wl.total) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_INVALID_ARG;
   int dev;
@@ -1028,8 +1027,7 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
   p.seqlens = seqlens_k;
   p.slopes = slopes;
   char* ws = static_cast<char*>(workspace);
-  p.prefix = reinterpret_cast<long long*>(ws + wl.prefix);
-  p.bad = reinterpret_cast<int*>(ws + wl.bad);
+  p.info = reinterpret_cast<int4*>(ws + wl.info);
   p.rec_o = reinterpret_cast<float*>(ws + wl.rec_o);
   p.rec_lse = reinterpret_cast<float*>(ws + wl.rec_lse);
   p.B = B;

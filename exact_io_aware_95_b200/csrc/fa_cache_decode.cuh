@@ -65,8 +65,8 @@ struct CDecParams {
   const uint8_t* vexp;
   const int* seqlens;     // [B] or nullptr
   const float* slopes;    // [H] or nullptr
-  long long* prefix;      // [B + 1] first unit of each entry, for the merge
-  int* bad;
+  int4* info;             // [group] {b, rb, first group, slot there} of the shared segment that ends
+                          // in the group's chunk; b = -1: none, -2: bad lengths
   float* rec_o;           // [CTA][2][8 NB][d]
   float* rec_lse;         // [CTA][2][8 NB]
   int B, Nq, Nk, H, Hkv, G;
@@ -90,8 +90,8 @@ struct CDecCfg {
   static constexpr int OFF_BAR = OFF_ACC + NW * 4 * ACC_LD * 4;
   static constexpr int BAR_FULL = 0, BAR_EMPTY = NSTAGE, NBAR = 2 * NSTAGE;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  // misc: abort flag, bad | scan [5] | b0 | base of b0 | per-warp ok [4]
-  static constexpr int SMEM_BYTES = OFF_MISC + 96 + 1024;
+  // misc: abort flag | per-warp ok [4]
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int THREADS = 32 * (NW + 1);
   static constexpr int CTAS = cdec_ctas_per_sm(NB);
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "CTAs per SM");
@@ -141,11 +141,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int n) -> uint32_t { return sbase + C::OFF_BAR + 8u * n; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
-  int* s_bad = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
-  long long* s_scan = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);  // [5]
-  int* s_b0 = reinterpret_cast<int*>(smem + C::OFF_MISC + 56);
-  long long* s_base0 = reinterpret_cast<long long*>(smem + C::OFF_MISC + 64);
-  int* s_ok = reinterpret_cast<int*>(smem + C::OFF_MISC + 72);  // [4] per compute warp
+  int* s_ok = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [4] per compute warp
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSTAGE; ++s) {
@@ -153,75 +149,70 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
       mbar_init(bar(C::BAR_EMPTY + s), C::NW * 32);
     }
     *abort_flag = 0;
-    *s_bad = 0;
     fence_mbar_init();
   }
-  __syncthreads();
+  if (warp == C::NW && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge waits for this grid's end itself
 
-  // ---- this CTA's units: every thread sums a run of entries, block scan
-  const int per = (p.B + C::THREADS - 1) / C::THREADS;
-  const int e0 = min(p.B, static_cast<int>(threadIdx.x) * per), e1 = min(p.B, e0 + per);
-  auto units = [&](int b) -> long long {
+  // ---- this CTA's units: every warp scans the lengths for itself, each lane a
+  // run of entries, so that no barrier stands before the first loads
+  const int per = (p.B + 31) >> 5;
+  const int e0 = min(p.B, lane * per), e1 = min(p.B, e0 + per);
+  auto units = [&](int b) -> int {  // fits 32 bits: the host checks
     const int L = cdec_len(p, b);
     if (L < 0 || L > p.Nk) return -1;
     const CDecRange r = cdec_range(p, L);
-    return static_cast<long long>(r.t1 - r.t0) * p.nrb;
+    return (r.t1 - r.t0) * p.nrb;
   };
   long long sum = 0;
   bool bad = false;
+#pragma unroll 4
   for (int b = e0; b < e1; ++b) {
-    const long long x = units(b);
-    if (x < 0) bad = true;
-    else sum += x;
+    const int x = units(b);
+    bad |= x < 0;
+    sum += max(x, 0);
   }
-  if (bad) *s_bad = 1;
+  const bool any_bad = __any_sync(0xffffffffu, bad);
   long long inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, inc, off);
     if (lane >= off) inc += x;
   }
-  if (lane == 31) s_scan[warp] = inc;
-  __syncthreads();
-  long long U = 0, base = inc - sum;
-  for (int w = 0; w < C::NW + 1; ++w) {
-    if (w < warp) base += s_scan[w];
-    U += s_scan[w];
-  }
-  const bool any_bad = *s_bad != 0;
+  const long long U = __shfl_sync(0xffffffffu, inc, 31);
   const long long chunk = (U + p.groups - 1) / p.groups;
-  const int hk = blockIdx.x % p.Hkv;  // this CTA's key head
-  const long long u0 = static_cast<long long>(blockIdx.x / p.Hkv) * chunk;
+  const int group = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;  // hk: this CTA's key head
+  const long long u0 = static_cast<long long>(group) * chunk;
   const long long u1 = min(U, u0 + chunk);
-  if (blockIdx.x == 0) {  // the merge kernel's copy
-    long long run = base;
-    for (int b = e0; b < e1; ++b) {
-      p.prefix[b] = run;
-      const long long x = units(b);
-      run += x < 0 ? 0 : x;
+  if (any_bad || u0 >= u1) {  // lengths contradict the cache: write nothing; or no units (uniform over the CTA)
+    if (hk == 0 && threadIdx.x == 0) {
+      p.info[group] = make_int4(any_bad ? -2 : -1, 0, 0, 0);
+      if (any_bad && group == 0) atomicOr(&g_fa_error_word, FA_DEVERR_BOUNDS);
     }
-    if (threadIdx.x == 0) {
-      p.prefix[p.B] = U;
-      *p.bad = any_bad;
-      if (any_bad) atomicOr(&g_fa_error_word, FA_DEVERR_BOUNDS);
-    }
+    return;
   }
-  if (any_bad) return;  // lengths contradict the cache: write nothing
-  if (u0 >= u1) return;  // uniform over the CTA
-  if (base <= u0 && u0 < base + sum) {
-    long long run = base;
-    int b = e0;
+  // the entry with unit u0, found by the lane whose run holds it
+  int b0 = 0;
+  long long base0 = inc - sum;
+  const bool mine = base0 <= u0 && u0 < inc;
+  if (mine) {
+    b0 = e0;
     for (;;) {
-      const long long x = units(b);
-      if (u0 < run + x) break;
-      run += x;
-      ++b;
+      const int x = units(b0);
+      if (u0 < base0 + x) break;
+      base0 += x;
+      ++b0;
     }
-    *s_b0 = b;
-    *s_base0 = run;
   }
-  __syncthreads();
+  {
+    const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    b0 = __shfl_sync(0xffffffffu, b0, from);
+    base0 = __shfl_sync(0xffffffffu, base0, from);
+  }
+  __syncthreads();  // the barriers are set up
 
   // Walk of the units [u0, u1), the same in both roles: segment (b, rb),
   // its tiles [r.t0, r.t1), the current tile tp.
@@ -230,13 +221,13 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     CDecRange r;
   };
   auto walk_begin = [&](Walk& w) {
-    w.b = *s_b0;
+    w.b = b0;
     w.L = cdec_len(p, w.b);
     w.r = cdec_range(p, w.L);
-    const long long rel = u0 - *s_base0;
+    const int rel = static_cast<int>(u0 - base0);
     const int T = w.r.t1 - w.r.t0;
-    w.rb = static_cast<int>(rel / T);
-    w.tp = w.r.t0 + static_cast<int>(rel % T);
+    w.rb = rel / T;
+    w.tp = w.r.t0 + rel % T;
   };
   auto walk_next = [&](Walk& w) {  // after the last tile of a segment, with units left
     if (++w.rb == p.nrb) {
@@ -253,13 +244,23 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   if (warp == C::NW) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
       Walk w;
       walk_begin(w);
       int issued = 0;
       bool ok = true;
       const int total = static_cast<int>(u1 - u0);
+      if (hk == 0) {  // for the merge: the segment that began before this chunk and ends in it
+        const int before = w.tp - w.r.t0;
+        int4 x = make_int4(-1, 0, 0, 0);
+        if (before > 0 && w.r.t1 - w.tp <= total) {
+          const long long s0 = u0 - before;
+          const int g0 = static_cast<int>(s0 / chunk);
+          // group g0's piece is its last one (slot 1) unless its chunk starts with the
+          // segment; every later group's piece is its first one (slot 0)
+          x = make_int4(w.b, w.rb, g0, g0 * chunk < s0 ? 1 : 0);
+        }
+        p.info[group] = x;
+      }
       for (int done = 0; ok && done < total; ++done) {
         const int st = issued % C::NSTAGE;
         if (!(ok = mbar_wait(bar(C::BAR_EMPTY + st), ((issued / C::NSTAGE) & 1) ^ 1u, abort_flag))) break;
@@ -620,89 +621,89 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   }
 }
 
-// One block per output row (batch entry, head, query): rows of entries whose
-// queries see no tile get O = 0, LSE = -inf; rows of segments shared by several
-// CTAs are combined from their records (the four warps take every fourth
-// record, four loads in flight each); the rest is written already.
-__global__ void __launch_bounds__(128) fa_cache_decode_merge_kernel(const CDecParams p, int D) {
-  __shared__ float s_w[kCacheDecodeGroupsMax];
-  __shared__ float s_red[4];
-  __shared__ float s_acc[3][128];
+// Merge: the blocks (group, key head; four rows) of groups in whose chunk a
+// segment ends that began in an earlier one combine that segment's records; the
+// four warps of a row take every fourth record.  The blocks also write O = 0,
+// LSE = -inf for entries whose queries see no tile, an entry at a time.
+__global__ void __launch_bounds__(512) fa_cache_decode_merge_kernel(const CDecParams p, int D) {
+  __shared__ float s_w[4][kCacheDecodeGroupsMax];
+  __shared__ float s_red[16];
+  __shared__ float s_acc[16][128];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the stream kernel has ended and its writes are visible
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (*p.bad) return;
-  const long long row = blockIdx.x;
-  const int qi = static_cast<int>(row % p.Nq);
-  const long long bh = row / p.Nq;
-  const int b = static_cast<int>(bh / p.H), h = static_cast<int>(bh % p.H);
-  const CDecRange rg = cdec_range(p, cdec_len(p, b));
-  const int T = rg.t1 - rg.t0;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<size_t>(b) * p.Nq + qi) * p.H + h) * D;
-  float* lse = p.lse + bh * p.Nq + qi;
-  if (T == 0) {
-    if (threadIdx.x < D) out[threadIdx.x] = __float2bfloat16(0.f);
-    if (threadIdx.x == 0) *lse = -INFINITY;
-    return;
+  const int group = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;
+  const int4 seg = p.info[group];
+  if (seg.x == -2) return;
+  if (hk == 0 && blockIdx.y == 0) {
+    for (int b = group; b < p.B; b += p.groups) {
+      const CDecRange rg = cdec_range(p, cdec_len(p, b));
+      if (rg.t0 < rg.t1) continue;
+      const int64_t rows = static_cast<int64_t>(p.Nq) * p.H;
+      uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + b * rows * D);
+      for (int64_t i = threadIdx.x; i < rows * D / 2; i += 512) o[i] = 0u;
+      for (int64_t i = threadIdx.x; i < rows; i += 512) p.lse[b * rows + i] = -INFINITY;
+    }
   }
-  const long long U = p.prefix[p.B];
-  const long long chunk = (U + p.groups - 1) / p.groups;
-  const int r = qi * p.G + h % p.G;  // row of its key head
-  const long long s0 = p.prefix[b] + static_cast<long long>(r / p.rpb) * T, s1 = s0 + T;
-  const int g0 = static_cast<int>(s0 / chunk), g1 = static_cast<int>((s1 - 1) / chunk);
-  if (g0 == g1) return;
-  const int n = g1 - g0 + 1;
-  // group g0's piece is its last one (slot 1) unless its chunk starts with the
-  // segment; every later group's piece is its first one (slot 0)
-  const int slot0 = static_cast<long long>(g0) * chunk < s0 ? 1 : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = warp >> 2, part = warp & 3;         // row of the block, share of its records
+  const int r_in = blockIdx.y * 4 + rr;              // row of the row block
+  const int r = seg.y * p.rpb + r_in;                // row of its key head
+  if (seg.x < 0 || seg.y * p.rpb + blockIdx.y * 4 >= p.rows) return;  // uniform over the block
+  const bool live = r < p.rows;
+  const int n = group - seg.z + 1;
   auto rec = [&](int k) -> size_t {
-    const size_t cta = static_cast<size_t>(g0 + k) * p.Hkv + h / p.G;
-    return (cta * 2 + (k == 0 ? slot0 : 0)) * p.rpb + r % p.rpb;
+    const size_t cta = static_cast<size_t>(seg.z + k) * p.Hkv + hk;
+    return (cta * 2 + (k == 0 ? seg.w : 0)) * p.rpb + r_in;
   };
   constexpr float kLog2ef = 1.4426950408889634f;
   float mx = -INFINITY;
-  for (int k = threadIdx.x; k < n; k += 128) {
-    const float x = p.rec_lse[rec(k)];
-    s_w[k] = x;
-    mx = fmaxf(mx, x);
-  }
+  if (live)
+    for (int k = part * 32 + lane; k < n; k += 128) {
+      const float x = p.rec_lse[rec(k)];
+      s_w[rr][k] = x;
+      mx = fmaxf(mx, x);
+    }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
   if (lane == 0) s_red[warp] = mx;
   __syncthreads();
-  mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  mx = fmaxf(fmaxf(s_red[4 * rr], s_red[4 * rr + 1]), fmaxf(s_red[4 * rr + 2], s_red[4 * rr + 3]));
   const float ref = mx == -INFINITY ? 0.f : mx;  // no record with a weight: all 0 (or NaN)
   float den = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
   const int cols = D / 32;
-#pragma unroll 4
-  for (int k = warp; k < n; k += 4) {
-    const float wk = ex2((s_w[k] - ref) * kLog2ef);
-    const float* o = p.rec_o + rec(k) * D + lane * cols;
-    den += wk;
-    if (cols == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(o);
-      acc[0] = fmaf(wk, v.x, acc[0]);
-      acc[1] = fmaf(wk, v.y, acc[1]);
-      acc[2] = fmaf(wk, v.z, acc[2]);
-      acc[3] = fmaf(wk, v.w, acc[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(o);
-      acc[0] = fmaf(wk, v.x, acc[0]);
-      acc[1] = fmaf(wk, v.y, acc[1]);
+  if (live) {
+#pragma unroll 8
+    for (int k = part; k < n; k += 4) {
+      const float wk = ex2((s_w[rr][k] - ref) * kLog2ef);
+      const float* o = p.rec_o + rec(k) * D + lane * cols;
+      den += wk;
+      if (cols == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        acc[0] = fmaf(wk, v.x, acc[0]);
+        acc[1] = fmaf(wk, v.y, acc[1]);
+        acc[2] = fmaf(wk, v.z, acc[2]);
+        acc[3] = fmaf(wk, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        acc[0] = fmaf(wk, v.x, acc[0]);
+        acc[1] = fmaf(wk, v.y, acc[1]);
+      }
     }
   }
   __syncthreads();  // s_red has been read
   if (lane == 0) s_red[warp] = den;
-  if (warp > 0)
-    for (int c = 0; c < cols; ++c) s_acc[warp - 1][lane * cols + c] = acc[c];
+  for (int c = 0; c < cols; ++c) s_acc[warp][lane * cols + c] = acc[c];
   __syncthreads();
-  if (warp > 0) return;
-  den = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  if (part > 0 || !live) return;
+  den = (s_red[4 * rr] + s_red[4 * rr + 1]) + (s_red[4 * rr + 2] + s_red[4 * rr + 3]);
   const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int qi = r / p.G, h = hk * p.G + r % p.G;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<size_t>(seg.x) * p.Nq + qi) * p.H + h) * D;
   for (int c = 0; c < cols; ++c) {
     const int x = lane * cols + c;
-    out[x] = __float2bfloat16((acc[c] + s_acc[0][x] + s_acc[1][x] + s_acc[2][x]) * inv);
+    out[x] = __float2bfloat16(((acc[c] + s_acc[4 * rr + 1][x]) + (s_acc[4 * rr + 2][x] + s_acc[4 * rr + 3][x])) * inv);
   }
-  if (lane == 0) *lse = den == 0.f ? -INFINITY : ref + lg2(den) * kLn2;
+  if (lane == 0)
+    p.lse[(static_cast<size_t>(seg.x) * p.H + h) * p.Nq + qi] = den == 0.f ? -INFINITY : ref + lg2(den) * kLn2;
 }
 
 }  // namespace fa

@@ -260,7 +260,7 @@ fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens
  * no key gets O = 0, LSE = -inf.  Rows that no query of the entry sees may hold
  * anything.  Lengths outside [0, Nk] and errors as in fa_decode_fwd.
  * workspace: ws_bytes >= fa_cache_decode_workspace_size(), 256-byte aligned (it
- * depends on B, Hkv and d only); calls that may run at the same time, captured ones
+ * depends on Hkv and d only); calls that may run at the same time, captured ones
  * among them, need workspaces of their own. */
 size_t fa_cache_decode_workspace_size(int B, int Nq, int Nk, int H, int Hkv, int d);
 fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
