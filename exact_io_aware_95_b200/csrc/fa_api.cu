@@ -564,15 +564,16 @@ fa_status cache_check(int B, int Nk, int Hkv, int d) {
 }
 
 struct CacheDecodeWs {
-  size_t info, rec_o, rec_lse, total;
+  size_t bad, info, rec_o, rec_lse, total;
 };
 CacheDecodeWs cache_decode_ws(int Hkv, int d) {
   CacheDecodeWs w;
   // CTAs of the stream kernel: at most one wave, or one group where Hkv is more
   const size_t ctas = Hkv > fa::kCacheDecodeGroupsMax ? Hkv : fa::kCacheDecodeGroupsMax;
   const size_t recs = ctas * 2 * 16;
-  w.info = 0;
-  w.rec_o = align256(static_cast<size_t>(fa::kCacheDecodeGroupsMax) * sizeof(int4));
+  w.bad = 0;
+  w.info = 256;
+  w.rec_o = w.info + align256(static_cast<size_t>(fa::kCacheDecodeGroupsMax) * sizeof(int4));
   w.rec_lse = w.rec_o + align256(recs * d * sizeof(float));
   w.total = w.rec_lse + align256(recs * sizeof(float));
   return w;
@@ -592,6 +593,8 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   p.nrb = (p.rows + p.rpb - 1) / p.rpb;
   const int wave = fa::cdec_ctas_per_sm(NB) * 148;
   p.groups = p.Hkv > wave ? 1 : wave / p.Hkv;
+  const int64_t segments = static_cast<int64_t>(p.B) * p.nrb;
+  p.by_segment = segments <= p.groups;
   // an entry's units and a CTA's share of all units are counted in 32 bits
   const int64_t tiles = static_cast<int64_t>(p.nrb) * ((p.Nk + 63) / 64);
   if (tiles >= 0x7fffffff || tiles * p.B / p.groups >= 0x7fffffff) return FA_ERR_INVALID_ARG;
@@ -602,12 +605,13 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.groups) * p.Hkv, p.rpb / 4);
-  cfg.blockDim = dim3(512);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.by_segment ? segments : p.groups) * p.Hkv, p.rows < p.rpb ? p.rows : p.rpb);
+  // records of a segment: about groups / segments.  Few: small blocks, all of them resident at once
+  cfg.blockDim = dim3(segments * 8 < p.groups ? 512 : 128);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_cache_decode_merge_kernel, p, D) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, fa::fa_cache_decode_merge_kernel<D>, p) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
@@ -1027,6 +1031,7 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
   p.seqlens = seqlens_k;
   p.slopes = slopes;
   char* ws = static_cast<char*>(workspace);
+  p.bad = reinterpret_cast<int*>(ws + wl.bad);
   p.info = reinterpret_cast<int4*>(ws + wl.info);
   p.rec_o = reinterpret_cast<float*>(ws + wl.rec_o);
   p.rec_lse = reinterpret_cast<float*>(ws + wl.rec_lse);

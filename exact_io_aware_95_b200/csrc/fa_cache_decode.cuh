@@ -65,12 +65,17 @@ struct CDecParams {
   const uint8_t* vexp;
   const int* seqlens;     // [B] or nullptr
   const float* slopes;    // [H] or nullptr
-  int4* info;             // [group] {b, rb, first group, slot there} of the shared segment that ends
-                          // in the group's chunk; b = -1: none, -2: bad lengths
+  int* bad;               // lengths outside the cache
+  // {b, rb, 2 x first group + slot there, last group} of a segment that several
+  // groups share, b = -1: not shared.  By segment b nrb + rb when there are no
+  // more segments than groups, else by the group in whose chunk it ends (one at
+  // most; the others end a segment they hold alone)
+  int4* info;
   float* rec_o;           // [CTA][2][8 NB][d]
   float* rec_lse;         // [CTA][2][8 NB]
   int B, Nq, Nk, H, Hkv, G;
   int rows, nrb, rpb;     // G Nq query rows per key head, blocks of rpb = 8 NB
+  int by_segment;
   int groups, causal, window;  // grid = groups * Hkv CTAs
   float scale_log2;       // scale log2 e          (no cap)
   float x_mul, cap_log2;  // scale / cap, cap log2 e
@@ -187,11 +192,12 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   const int group = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;  // hk: this CTA's key head
   const long long u0 = static_cast<long long>(group) * chunk;
   const long long u1 = min(U, u0 + chunk);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.bad = any_bad;
+    if (any_bad) atomicOr(&g_fa_error_word, FA_DEVERR_BOUNDS);
+  }
   if (any_bad || u0 >= u1) {  // lengths contradict the cache: write nothing; or no units (uniform over the CTA)
-    if (hk == 0 && threadIdx.x == 0) {
-      p.info[group] = make_int4(any_bad ? -2 : -1, 0, 0, 0);
-      if (any_bad && group == 0) atomicOr(&g_fa_error_word, FA_DEVERR_BOUNDS);
-    }
+    if (!any_bad && !p.by_segment && hk == 0 && threadIdx.x == 0) p.info[group] = make_int4(-1, 0, 0, 0);
     return;
   }
   // the entry with unit u0, found by the lane whose run holds it
@@ -249,17 +255,21 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
       int issued = 0;
       bool ok = true;
       const int total = static_cast<int>(u1 - u0);
-      if (hk == 0) {  // for the merge: the segment that began before this chunk and ends in it
-        const int before = w.tp - w.r.t0;
+      // for the merge: the first segment, when it began before this chunk and ends in it
+      const int before = w.tp - w.r.t0;
+      const bool ends = w.r.t1 - w.tp <= total;
+      int ended = 0;  // segments completed in this chunk; later ones are whole
+      if (hk == 0) {
         int4 x = make_int4(-1, 0, 0, 0);
-        if (before > 0 && w.r.t1 - w.tp <= total) {
+        if (before > 0 && ends) {
           const long long s0 = u0 - before;
           const int g0 = static_cast<int>(s0 / chunk);
           // group g0's piece is its last one (slot 1) unless its chunk starts with the
           // segment; every later group's piece is its first one (slot 0)
-          x = make_int4(w.b, w.rb, g0, g0 * chunk < s0 ? 1 : 0);
+          x = make_int4(w.b, w.rb, 2 * g0 + (g0 * chunk < s0 ? 1 : 0), group);
         }
-        p.info[group] = x;
+        if (!p.by_segment) p.info[group] = x;
+        else if (ends) p.info[w.b * p.nrb + w.rb] = x;
       }
       for (int done = 0; ok && done < total; ++done) {
         const int st = issued % C::NSTAGE;
@@ -273,7 +283,10 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           tma_load_4d(dst + C::TILE + x * 32 * D, &tmV, bar(C::BAR_FULL + st), 0, hk, row + 32 * x, w.b);
         }
         ++issued;
-        if (++w.tp == w.r.t1 && done + 1 < total) walk_next(w);
+        if (++w.tp == w.r.t1) {
+          if (hk == 0 && p.by_segment && ended++ > 0) p.info[w.b * p.nrb + w.rb] = make_int4(-1, 0, 0, 0);
+          if (done + 1 < total) walk_next(w);
+        }
       }
       if (*abort_flag) {  // let the copies in flight land before the CTA exits
         for (int n = 0; n < C::NSTAGE && n < issued; ++n) {
@@ -552,68 +565,73 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
     const bool whole = w.tp == w.r.t0 && n == w.r.t1 - w.r.t0;  // the piece is the whole segment
     const int slot = done == 0 ? 0 : 1;
     const int nrows = min(C::R, p.rows - w.rb * C::R);
+    // rows 4 x4 .. 4 x4 + 3 at a time: lanes t = 2 (x4 & 1), + 1.  Not unrolled:
+    // this runs once or twice a CTA, where fetching its instructions costs more
+    // than the selects (four copies of it took 9 us of a 31 us call)
+#pragma unroll 1
+    for (int r0 = 0; r0 < nrows; r0 += 4) {
+      const bool hi = NB == 2 && r0 >= 8;
+      if ((t >> 1) == ((r0 >> 2) & 1)) {
 #pragma unroll
-    for (int x4 = 0; x4 < 2 * NB; ++x4) {  // rows 4 x4 .. 4 x4 + 3: lanes t = 2 (x4 & 1), + 1
-      const int r0 = 4 * x4, nb = x4 >> 1;
-      if (r0 < nrows) {
-        if ((t >> 1) == (x4 & 1)) {
+        for (int e = 0; e < 2; ++e) {
+          const int row = (r0 & 8) + 2 * t + e;
+          const float mow = hi ? mo[2 * (NB - 1) + e] : mo[e];
+          float M = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = 2 * nb + e, row = 8 * nb + 2 * t + e;
-            float M = -INFINITY;
+          for (int y = 0; y < C::NW; ++y) M = fmaxf(M, sMl[(C::NW + y) * C::R + row]);
+          // this warp's output factor: 2^(mo_w - mo), 0 when it saw nothing
+          const float f = mow == -INFINITY ? 0.f : ex2(mow - M);
+          float* dst = sAcc + (warp * 4 + (row & 3)) * C::ACC_LD + g * (D / 8);
 #pragma unroll
-            for (int y = 0; y < C::NW; ++y) M = fmaxf(M, sMl[(C::NW + y) * C::R + row]);
-            // this warp's output factor: 2^(mo_w - mo), 0 when it saw nothing
-            const float f = mo[x] == -INFINITY ? 0.f : ex2(mo[x] - M);
-            float* dst = sAcc + (warp * 4 + (row & 3)) * C::ACC_LD + g * (D / 8);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-              *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nb][e] * f, acc[i][nb][2 + e] * f);
-          }
+          for (int i = 0; i < MT; ++i)
+            *reinterpret_cast<float2*>(dst + 2 * i) = make_float2((hi ? acc[i][NB - 1][e] : acc[i][0][e]) * f,
+                                                                  (hi ? acc[i][NB - 1][2 + e] : acc[i][0][2 + e]) * f);
         }
-        named_bar_sync(1, C::NW * 32);
-        const int row = r0 + warp;  // warp = row of the pass
-        if (row < nrows) {
-          float M = -INFINITY, MO = -INFINITY, lsum = 0.f;
-#pragma unroll
-          for (int y = 0; y < C::NW; ++y) {
-            M = fmaxf(M, sMl[y * C::R + row]);
-            MO = fmaxf(MO, sMl[(C::NW + y) * C::R + row]);
-          }
-#pragma unroll
-          for (int y = 0; y < C::NW; ++y) {
-            const float mw = sMl[y * C::R + row], lw = sMl[(2 * C::NW + y) * C::R + row];
-            // a warp without a maximum has seen nothing (l = 0) or NaN only (l = NaN)
-            lsum += mw == -INFINITY ? lw : lw * ex2(mw - M);
-          }
-          const float inv = lsum == 0.f ? 0.f : ex2(MO - M) / lsum;
-          const float lse = lsum == 0.f ? -INFINITY : (M + lg2(lsum)) * kLn2;
-          const int r = w.rb * C::R + row, qi = r / p.G, h = hk * p.G + r % p.G;
-          const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + slot) * C::R + row;
-          for (int c = lane * 2; c < D; c += 64) {
-            float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-            for (int y = 0; y < C::NW; ++y) {
-              const float2 v = *reinterpret_cast<const float2*>(sAcc + (y * 4 + warp) * C::ACC_LD + c);
-              a0 += v.x;
-              a1 += v.y;
-            }
-            a0 *= inv;
-            a1 *= inv;
-            if (whole)
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                           ((static_cast<size_t>(w.b) * p.Nq + qi) * p.H + h) * D + c) =
-                  pack_bf16x2(a0, a1);
-            else
-              *reinterpret_cast<float2*>(p.rec_o + rec * D + c) = make_float2(a0, a1);
-          }
-          if (lane == 0) {
-            if (whole) p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.Nq + qi] = lse;
-            else p.rec_lse[rec] = lse;
-          }
-        }
-        named_bar_sync(1, C::NW * 32);
       }
+      named_bar_sync(1, C::NW * 32);
+      const int row = r0 + warp;  // warp = row of the pass
+      if (row < nrows) {
+        float M = -INFINITY, MO = -INFINITY, lsum = 0.f;
+#pragma unroll
+        for (int y = 0; y < C::NW; ++y) {
+          M = fmaxf(M, sMl[y * C::R + row]);
+          MO = fmaxf(MO, sMl[(C::NW + y) * C::R + row]);
+        }
+#pragma unroll
+        for (int y = 0; y < C::NW; ++y) {
+          const float mw = sMl[y * C::R + row], lw = sMl[(2 * C::NW + y) * C::R + row];
+          // a warp without a maximum has seen nothing (l = 0) or NaN only (l = NaN)
+          lsum += mw == -INFINITY ? lw : lw * ex2(mw - M);
+        }
+        const float inv = lsum == 0.f ? 0.f : __fdividef(ex2(MO - M), lsum);
+        const float lse = lsum == 0.f ? -INFINITY : (M + lg2(lsum)) * kLn2;
+        const int r = w.rb * C::R + row, qi = r / p.G, h = hk * p.G + r % p.G;
+        const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + slot) * C::R + row;
+        constexpr int PL = D / 32;  // columns per lane, PL at a time
+        float a[PL];
+#pragma unroll
+        for (int c = 0; c < PL; ++c) a[c] = 0.f;
+#pragma unroll
+        for (int y = 0; y < C::NW; ++y)
+#pragma unroll
+          for (int c = 0; c < PL; c += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(sAcc + (y * 4 + warp) * C::ACC_LD + lane * PL + c);
+            a[c] += v.x;
+            a[c + 1] += v.y;
+          }
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) +
+                             ((static_cast<size_t>(w.b) * p.Nq + qi) * p.H + h) * D + lane * PL;
+#pragma unroll
+        for (int c = 0; c < PL; c += 2) {
+          if (whole) *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(a[c] * inv, a[c + 1] * inv);
+          else *reinterpret_cast<float2*>(p.rec_o + rec * D + lane * PL + c) = make_float2(a[c] * inv, a[c + 1] * inv);
+        }
+        if (lane == 0) {
+          float* dst = whole ? p.lse + (static_cast<size_t>(w.b) * p.H + h) * p.Nq + qi : p.rec_lse + rec;
+          *dst = lse;
+        }
+      }
+      named_bar_sync(1, C::NW * 32);
     }
     done += n;
     w.tp += n;
@@ -621,89 +639,134 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   }
 }
 
-// Merge: the blocks (group, key head; four rows) of groups in whose chunk a
-// segment ends that began in an earlier one combine that segment's records; the
-// four warps of a row take every fourth record.  The blocks also write O = 0,
-// LSE = -inf for entries whose queries see no tile, an entry at a time.
-__global__ void __launch_bounds__(512) fa_cache_decode_merge_kernel(const CDecParams p, int D) {
-  __shared__ float s_w[4][kCacheDecodeGroupsMax];
-  __shared__ float s_red[16];
-  __shared__ float s_acc[16][128];
+// Merge of the records of segments that several groups share: one block per
+// (segment, key head; row), or, where there are more segments than groups, per
+// (group, key head; row) for the one such segment that may end in its chunk.
+// The block's warps take the records in turn, eight in flight each, under a
+// maximum of their own, and join at the end.  The blocks also write O = 0,
+// LSE = -inf for entries whose queries see no tile.  Bound by the latency of
+// three dependent loads and by the launch of its blocks (per group always, the
+// 4736 blocks of 148 records shared by two segments took 16 us; four rows a
+// block 14 us).
+template <int D>
+__global__ void __launch_bounds__(512) fa_cache_decode_merge_kernel(const CDecParams p) {
+  __shared__ float s_m[16], s_den[16];
+  __shared__ float s_acc[16][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the stream kernel has ended and its writes are visible
-  const int group = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;
-  const int4 seg = p.info[group];
-  if (seg.x == -2) return;
-  if (hk == 0 && blockIdx.y == 0) {
-    for (int b = group; b < p.B; b += p.groups) {
+  const int idx = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;
+  const int4 seg = p.info[idx];
+  if (*p.bad) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int r_in = blockIdx.y;  // row of the row block
+  if (p.by_segment) {
+    const int b = idx / p.nrb, r = (idx % p.nrb) * p.rpb + r_in;
+    const CDecRange rg = cdec_range(p, cdec_len(p, b));
+    if (rg.t0 >= rg.t1) {  // nobody wrote info for this segment
+      if (r < p.rows) {
+        const int qi = r / p.G, h = hk * p.G + r % p.G;
+        uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
+                                                  ((static_cast<size_t>(b) * p.Nq + qi) * p.H + h) * D);
+        if (threadIdx.x < D / 2) o[threadIdx.x] = 0u;
+        if (threadIdx.x == 0) p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + qi] = -INFINITY;
+      }
+      return;
+    }
+  } else if (hk == 0 && r_in == 0) {
+#pragma unroll 1
+    for (int b = idx; b < p.B; b += p.groups) {
       const CDecRange rg = cdec_range(p, cdec_len(p, b));
       if (rg.t0 < rg.t1) continue;
       const int64_t rows = static_cast<int64_t>(p.Nq) * p.H;
       uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + b * rows * D);
-      for (int64_t i = threadIdx.x; i < rows * D / 2; i += 512) o[i] = 0u;
-      for (int64_t i = threadIdx.x; i < rows; i += 512) p.lse[b * rows + i] = -INFINITY;
+#pragma unroll 1
+      for (int64_t i = threadIdx.x; i < rows * D / 2; i += blockDim.x) o[i] = 0u;
+#pragma unroll 1
+      for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) p.lse[b * rows + i] = -INFINITY;
     }
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = warp >> 2, part = warp & 3;         // row of the block, share of its records
-  const int r_in = blockIdx.y * 4 + rr;              // row of the row block
-  const int r = seg.y * p.rpb + r_in;                // row of its key head
-  if (seg.x < 0 || seg.y * p.rpb + blockIdx.y * 4 >= p.rows) return;  // uniform over the block
-  const bool live = r < p.rows;
-  const int n = group - seg.z + 1;
-  auto rec = [&](int k) -> size_t {
-    const size_t cta = static_cast<size_t>(seg.z + k) * p.Hkv + hk;
-    return (cta * 2 + (k == 0 ? seg.w : 0)) * p.rpb + r_in;
-  };
+  const int r = seg.y * p.rpb + r_in;    // row of its key head
+  if (seg.x < 0 || r >= p.rows) return;  // uniform over the block
+  const int g0 = seg.z >> 1, slot0 = seg.z & 1, n = seg.w - g0 + 1;
+  constexpr int PL = D / 32;  // columns per lane
   constexpr float kLog2ef = 1.4426950408889634f;
-  float mx = -INFINITY;
-  if (live)
-    for (int k = part * 32 + lane; k < n; k += 128) {
-      const float x = p.rec_lse[rec(k)];
-      s_w[rr][k] = x;
-      mx = fmaxf(mx, x);
-    }
+  float m = -INFINITY, den = 0.f, acc[PL];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if (lane == 0) s_red[warp] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_red[4 * rr], s_red[4 * rr + 1]), fmaxf(s_red[4 * rr + 2], s_red[4 * rr + 3]));
-  const float ref = mx == -INFINITY ? 0.f : mx;  // no record with a weight: all 0 (or NaN)
-  float den = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const int cols = D / 32;
-  if (live) {
-#pragma unroll 8
-    for (int k = part; k < n; k += 4) {
-      const float wk = ex2((s_w[rr][k] - ref) * kLog2ef);
-      const float* o = p.rec_o + rec(k) * D + lane * cols;
-      den += wk;
-      if (cols == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] = fmaf(wk, v.x, acc[0]);
-        acc[1] = fmaf(wk, v.y, acc[1]);
-        acc[2] = fmaf(wk, v.z, acc[2]);
-        acc[3] = fmaf(wk, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] = fmaf(wk, v.x, acc[0]);
-        acc[1] = fmaf(wk, v.y, acc[1]);
+  for (int c = 0; c < PL; ++c) acc[c] = 0.f;
+#pragma unroll 1
+  for (int k0 = warp; k0 < n; k0 += 8 * nw) {
+    float ls[8], v[8][PL];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + nw * i;
+      ls[i] = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < PL; ++c) v[i][c] = 0.f;
+      if (k < n) {
+        const size_t cta = static_cast<size_t>(g0 + k) * p.Hkv + hk;
+        const size_t rec = (cta * 2 + (k == 0 ? slot0 : 0)) * p.rpb + r_in;
+        ls[i] = p.rec_lse[rec] * kLog2ef;
+        const float* o = p.rec_o + rec * D + lane * PL;
+        if constexpr (PL == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o);
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+          v[i][2] = x.z;
+          v[i][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o);
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+        }
       }
     }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ls[i]);
+    const float ref = mn == -INFINITY ? 0.f : mn;  // no weight yet: all 0 (or NaN)
+    const float al = m == -INFINITY ? 1.f : ex2(m - ref);
+    m = mn;
+    den *= al;
+#pragma unroll
+    for (int c = 0; c < PL; ++c) acc[c] *= al;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float wk = ex2(ls[i] - ref);
+      den += wk;
+#pragma unroll
+      for (int c = 0; c < PL; ++c) acc[c] = fmaf(wk, v[i][c], acc[c]);
+    }
   }
-  __syncthreads();  // s_red has been read
-  if (lane == 0) s_red[warp] = den;
-  for (int c = 0; c < cols; ++c) s_acc[warp][lane * cols + c] = acc[c];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_den[warp] = den;
+  }
+#pragma unroll
+  for (int c = 0; c < PL; ++c) s_acc[warp][lane * PL + c] = acc[c];
   __syncthreads();
-  if (part > 0 || !live) return;
-  den = (s_red[4 * rr] + s_red[4 * rr + 1]) + (s_red[4 * rr + 2] + s_red[4 * rr + 3]);
+  if (warp > 0) return;
+  float mx = -INFINITY;
+#pragma unroll 4
+  for (int y = 0; y < nw; ++y) mx = fmaxf(mx, s_m[y]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  den = 0.f;
+#pragma unroll
+  for (int c = 0; c < PL; ++c) acc[c] = 0.f;
+#pragma unroll 4
+  for (int y = 0; y < nw; ++y) {
+    // a share without a maximum has weight 0, or NaN sums that stay NaN
+    const float f = s_m[y] == -INFINITY ? 1.f : ex2(s_m[y] - ref);
+    den = fmaf(f, s_den[y], den);
+#pragma unroll
+    for (int c = 0; c < PL; ++c) acc[c] = fmaf(f, s_acc[y][lane * PL + c], acc[c]);
+  }
   const float inv = den == 0.f ? 0.f : 1.f / den;
   const int qi = r / p.G, h = hk * p.G + r % p.G;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<size_t>(seg.x) * p.Nq + qi) * p.H + h) * D;
-  for (int c = 0; c < cols; ++c) {
-    const int x = lane * cols + c;
-    out[x] = __float2bfloat16(((acc[c] + s_acc[4 * rr + 1][x]) + (s_acc[4 * rr + 2][x] + s_acc[4 * rr + 3][x])) * inv);
-  }
+  __nv_bfloat16* out =
+      static_cast<__nv_bfloat16*>(p.o) + ((static_cast<size_t>(seg.x) * p.Nq + qi) * p.H + h) * D + lane * PL;
+#pragma unroll
+  for (int c = 0; c < PL; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
   if (lane == 0)
-    p.lse[(static_cast<size_t>(seg.x) * p.H + h) * p.Nq + qi] = den == 0.f ? -INFINITY : ref + lg2(den) * kLn2;
+    p.lse[(static_cast<size_t>(seg.x) * p.H + h) * p.Nq + qi] = den == 0.f ? -INFINITY : (ref + lg2(den)) * kLn2;
 }
 
 }  // namespace fa
