@@ -11,6 +11,7 @@ cu_seqlens int32 [nseq + 1] on the device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -99,13 +100,25 @@ def _check(status: int, where: str):
         raise FaError(status, where)
 
 
+# The current stream's handle of a device, without building a torch.cuda.Stream
+# object on every call (2 us of a short call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _on(t: torch.Tensor):
     """Make the tensors' device current for the call: the library launches on
     the calling thread's current device and stream."""
+    if torch.cuda.current_device() == t.get_device():
+        return _NOTHING
     return torch.cuda.device(t.device)
 
 
@@ -124,6 +137,8 @@ def _need_shape(t, name: str, dtype, shape):
     """`t` must be a contiguous tensor of `dtype` and exactly `shape`:
     the kernels index every buffer from the sizes of q, so a smaller one
     would be read or written past its end."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return
     _need(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -141,6 +156,9 @@ def _need_workspace(ws, need: int):
 def _same_device(*ts):
     """Every tensor on one CUDA device (checked after dtypes and shapes, right
     before the call)."""
+    at = ts[0].get_device()  # -1: not on a GPU
+    if at >= 0 and all([t.get_device() == at for t in ts]):
+        return
     dev = ts[0].device
     for t in ts:
         if not t.is_cuda:
