@@ -45,7 +45,7 @@ def nvcc() -> str:
 
 
 def command(out: str = LIB_PATH, defines=(), sources=None) -> list:
-    cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17", "-split-compile=0",
+    cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
            "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"), "-o", out]
     cmd += ["-D" + d for d in defines]
     return cmd + list(sources or SOURCES)

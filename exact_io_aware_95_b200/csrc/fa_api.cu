@@ -497,6 +497,34 @@ fa_status mod_check(int B, int N, int H, int Hkv, int d, float scale, float soft
   return FA_OK;
 }
 
+// Parts that the heads of a group are split into in the backward pass: as few
+// as give the persistent CTAs enough items.  Under a causal mask the longest
+// item meets T query tiles per head and an SM's share of all items is about
+// T (T + 1) / 2 B H / 148 of them; the split keeps the former below half the
+// latter twice over: parts >= 296 / ((T + 1) B Hkv), a divisor of the group.
+int mod_bwd_parts(int B, int N, int H, int Hkv) {
+  const int G = H / Hkv, T = (N + 127) / 128;
+  const int64_t per_part = static_cast<int64_t>(T + 1) * B * Hkv;
+  for (int parts = 1; parts < G; ++parts)
+    if (G % parts == 0 && per_part * parts >= 296) return parts;
+  return G;
+}
+
+struct ModBwdWs {
+  size_t dvec, dk_part, dv_part, total;
+};
+ModBwdWs mod_bwd_ws(int B, int N, int H, int Hkv, int d) {
+  ModBwdWs w;
+  const size_t rows = static_cast<size_t>(B) * N;
+  const int parts = mod_bwd_parts(B, N, H, Hkv);
+  const size_t part = parts > 1 ? align256(rows * Hkv * parts * d * sizeof(float)) : 0;
+  w.dvec = align256(rows * H * d * sizeof(float));
+  w.dk_part = w.dvec + align256(rows * H * sizeof(float));
+  w.dv_part = w.dk_part + part;
+  w.total = w.dv_part + part;
+  return w;
+}
+
 template <int D, bool CAP, bool BIAS>
 fa_status launch_mod_fwd(int dev, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const fa::ModFwdParams& p, cudaStream_t s) {
@@ -527,15 +555,18 @@ fa_status launch_mod_bwd(int dev, const CUtensorMap& mq, const CUtensorMap& mk, 
   constexpr int smem = fa::ModBwdCfg<D>::SMEM_BYTES;
   fa_status st = ensure_smem(kern, dev, smem, done, fa::BwdCfg<D>::LAUNCH_REGS);
   if (st != FA_OK) return st;
-  const int64_t grid = static_cast<int64_t>(p.T) * p.B * p.Hkv;
+  const int64_t grid = static_cast<int64_t>(p.T) * p.B * p.Hv;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.H * ((p.N + 31) / 32);
-  if (grid > 0x7fffffff || blocks > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  const int64_t red = (static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4) + 255) / 256;
+  if (grid > 0x7fffffff || blocks > 0x7fffffff || red > 0x7fffffff) return FA_ERR_INVALID_ARG;
   mark_launch(s);
   fa::fa_mod_bwd_preprocess_kernel<D><<<preprocess_blocks(dev), 256, 0, s>>>(p);
   if ((st = launch_status(s)) != FA_OK) return st;
   kern<<<static_cast<unsigned>(grid), fa::BwdCfg<D>::THREADS, smem, s>>>(mq, mk, mv, mdo, p);
   if ((st = launch_status(s)) != FA_OK) return st;
   fa::fa_bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(conv);
+  if ((st = launch_status(s)) != FA_OK || !p.dk_part) return st;
+  fa::fa_mod_bwd_reduce_kernel<<<dim3(static_cast<unsigned>(red), 2), 256, 0, s>>>(p, D);
   return launch_status(s);
 }
 
@@ -865,9 +896,9 @@ fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void*
                  : dispatch_mod_fwd<128>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, p, s);
 }
 
-size_t fa_mod_bwd_workspace_size(int B, int N, int H, int d) {
-  if (!valid_plan_shape(B, N)) return 0;
-  return fa_bwd_workspace_size(B, N, H, d);
+size_t fa_mod_bwd_workspace_size(int B, int N, int H, int Hkv, int d) {
+  if (!valid_plan_shape(B, N) || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return mod_bwd_ws(B, N, H, Hkv, d).total;
 }
 
 fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o, const void* o_low, const float* lse,
@@ -882,7 +913,8 @@ fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o,
   int dev;
   fa_status st = mod_check(B, N, H, Hkv, d, scale, softcap, plan, slopes);
   if (st != FA_OK) return st;
-  if (ws_bytes < ws_bytes_for(static_cast<int64_t>(B) * N, H, d)) return FA_ERR_WORKSPACE;
+  const ModBwdWs wl = mod_bwd_ws(B, N, H, Hkv, d);
+  if (ws_bytes < wl.total) return FA_ERR_WORKSPACE;
   if ((st = current_device(&dev)) != FA_OK) return st;
   CUtensorMap mq, mk, mv, mdo;
   if ((st = make_map_bf16(&mq, q, d, H, N, B, 128)) != FA_OK) return st;
@@ -897,9 +929,14 @@ fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o,
   p.slopes = slopes;
   p.dk = dk;
   p.dv = dv;
-  p.dq_acc = static_cast<float*>(workspace);
-  p.dvec = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                    align256(static_cast<size_t>(B) * N * H * d * sizeof(float)));
+  char* ws = static_cast<char*>(workspace);
+  p.dq_acc = reinterpret_cast<float*>(ws);
+  p.dvec = reinterpret_cast<float*>(ws + wl.dvec);
+  const int parts = mod_bwd_parts(B, N, H, Hkv);
+  p.dk_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.dk_part) : nullptr;
+  p.dv_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.dv_part) : nullptr;
+  p.Hv = Hkv * parts;
+  p.hs = H / p.Hv;
   p.plan = plan_view(plan, B, N);
   p.B = B;
   p.N = N;
@@ -907,7 +944,7 @@ fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o,
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.T = (N + 127) / 128;
-  p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.G, static_cast<int64_t>(B) * Hkv);  // Q, dO, dQ acc
+  p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.hs, static_cast<int64_t>(B) * p.Hv);  // Q, dO, dQ acc
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.x_mul = softcap > 0.f ? scale / softcap : 0.f;

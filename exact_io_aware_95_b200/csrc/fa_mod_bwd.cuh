@@ -17,7 +17,12 @@
 //     query tiles of the mask plan's range for that key tile, for every query
 //     head of the group in turn, so dK and dV of a shared key head accumulate
 //     in tensor memory over the whole group: no atomics, no second pass, a
-//     fixed order.  A key tile no query sees is stored as zero;
+//     fixed order.  A key tile no query sees is stored as zero.  Where that
+//     makes too few items for the SMs (few key heads, short sequences) the host
+//     splits each group's heads over several items; those store fp32 partial
+//     sums, and a last kernel adds them in a fixed order: 2 x 8 heads on one key
+//     head x 2047 tokens, window 512, takes 32 items whole (181 us) and 256
+//     split;
 //   - D takes O with its rounding residual when the caller has it: with O in
 //     bf16 alone, rows that one key dominates (P near 1, dP - D near 0) lose
 //     bits: relative error of dQ 5.2e-3 against 3.0e-3 at q = 8 N(0,1),
@@ -40,12 +45,15 @@ struct ModBwdParams {
   const float* slopes;  // [H], BIAS
   void* dk;
   void* dv;
+  float* dk_part;       // fp32 [B, N, Hv, d] partial dK (unscaled) and dV when a
+  float* dv_part;       // group's heads are split, else nullptr
   float* dq_acc;        // layout: dq_acc_index4()
   float* dvec;          // fp32 D [B, H, N]
   PlanView plan;
   int B, N, H, Hkv, G;
+  int Hv, hs;           // items of a key tile in a batch entry, hs = H / Hv query heads each
   int T;                // ceil(N / 128)
-  int group;            // key heads per scheduling group
+  int group;            // (entry, Hv) pairs per scheduling group
   float scale, scale_log2, x_mul, cap_log2;
 };
 
@@ -113,28 +121,29 @@ struct ModBwdCfg : BwdCfg<D> {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-// One work item: (128-key tile j, batch entry, key head).  Key heads go in
+// One work item: (128-key tile j, batch entry, heads of a key head).  They go in
 // groups of p.group, sized on the host so that a group's Q, dO and dQ
 // accumulator rows stay in L2; inside a group early key tiles go first (under
 // a causal mask they meet the most queries).
 struct ModBwdItem {
-  int hk, b, k0, i_begin, ni, niter;  // niter = ni query tiles x G heads
+  int hv, hk, b, k0, i_begin, ni, niter;  // niter = ni query tiles x hs heads
 };
 
 __device__ __forceinline__ void mod_bwd_item(const ModBwdParams& p, int c, ModBwdItem& it) {
-  const int nbh = p.B * p.Hkv;
+  const int nbh = p.B * p.Hv;
   const int g = c / (p.group * p.T);
   const int gs = min(p.group, nbh - g * p.group);
   const int cidx = c - g * p.group * p.T;
   const int bh = g * p.group + cidx % gs;
   const int j = cidx / gs;
-  it.hk = bh % p.Hkv;
-  it.b = bh / p.Hkv;
+  it.hv = bh % p.Hv;
+  it.hk = it.hv * p.hs / p.G;
+  it.b = bh / p.Hv;
   it.k0 = 128 * j;
   const PlanKTile kt = p.plan.kt[static_cast<size_t>(it.b) * p.T + j];
-  it.i_begin = kt.qbeg;
-  it.ni = kt.qend - kt.qbeg;
-  it.niter = it.ni * p.G;
+  it.i_begin = max(kt.qbeg, 0);  // clamped as in the forward pass
+  it.ni = max(min(kt.qend, p.T) - it.i_begin, 0);
+  it.niter = it.ni * p.hs;
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(512, 1)
             tma_load_4d(sbase + C::OFF_V + c * 16384, &tmV, bar(C::BAR_KV), c * 64, I.hk, I.k0, I.b);
           }
           ++nitems;
-          int h = I.hk * p.G, i = 0;  // query head and tile of the walk
+          int h = I.hv * p.hs, i = 0;  // query head and tile of the walk
           for (int it = 0; it < I.niter; ++it, ++gt) {
             const int st = gt % C::NSTAGE;
             const uint32_t ph = (gt / C::NSTAGE) & 1;
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(512, 1)
           sv = lo | (max(hi - lo, 0) << 16);
         }
       };
-      int h = I.hk * p.G, i = 0;
+      int h = I.hv * p.hs, i = 0;
       if (I.niter > 0) fetch(h, 128 * I.i_begin);
       for (int it = 0; it < I.niter; ++it) {
         const uint32_t par = (gt0 + it) & 1;
@@ -486,21 +495,32 @@ __global__ void __launch_bounds__(512, 1)
           uint32_t s[32];
           tmem_ld32(lane_base + C::TM_S + 32 * cc, s);
           tmem_wait_ld(s);
-          bool small = true;
-          if constexpr (CAP) {
+          if constexpr (CAP) {  // s becomes t = tanh(x / cap)
             float ax = 0.f;
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
               ax = fmax3(ax, fabsf(__uint_as_float(s[e])), fabsf(__uint_as_float(s[e + 1])));
-            small = __all_sync(0xffffffffu, ax * fabsf(p.x_mul) <= kTanhRange);
+            if (__all_sync(0xffffffffu, ax * fabsf(p.x_mul) <= kTanhRange)) {
+              const uint64_t xm2 = f2_pack(p.x_mul, p.x_mul);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float a, b;
+                f2_unpack(tanh2_poly(fmul2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), xm2)), a, b);
+                s[e] = __float_as_uint(a);
+                s[e + 1] = __float_as_uint(b);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(tanh_any(__uint_as_float(s[e]) * p.x_mul));
+            }
           }
           uint32_t pw[16];
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
             const float4 l4 = sLSE4[8 * cc + m];
             const int qa = 32 * cc + 4 * m;
-            uint64_t s01 = f2_pack(__uint_as_float(s[4 * m + 0]), __uint_as_float(s[4 * m + 1]));
-            uint64_t s23 = f2_pack(__uint_as_float(s[4 * m + 2]), __uint_as_float(s[4 * m + 3]));
+            const uint64_t s01 = f2_pack(__uint_as_float(s[4 * m + 0]), __uint_as_float(s[4 * m + 1]));
+            const uint64_t s23 = f2_pack(__uint_as_float(s[4 * m + 2]), __uint_as_float(s[4 * m + 3]));
             uint64_t l01 = f2_pack(l4.x, l4.y), l23 = f2_pack(l4.z, l4.w);
             if constexpr (BIAS) {
               l01 = fadd2(l01, kb2);
@@ -513,19 +533,7 @@ __global__ void __launch_bounds__(512, 1)
             }
             uint64_t z01, z23;
             if constexpr (CAP) {
-              const uint64_t xm2 = f2_pack(p.x_mul, p.x_mul), cl2 = f2_pack(p.cap_log2, p.cap_log2);
-              s01 = fmul2(s01, xm2);
-              s23 = fmul2(s23, xm2);
-              if (small) {
-                s01 = tanh2_poly(s01);
-                s23 = tanh2_poly(s23);
-              } else {
-                float a, b;
-                f2_unpack(s01, a, b);
-                s01 = f2_pack(tanh_any(a), tanh_any(b));
-                f2_unpack(s23, a, b);
-                s23 = f2_pack(tanh_any(a), tanh_any(b));
-              }
+              const uint64_t cl2 = f2_pack(p.cap_log2, p.cap_log2);
               z01 = ffma2(s01, cl2, l01);
               z23 = ffma2(s23, cl2, l23);
             } else {
@@ -625,6 +633,15 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) a[e] = 0u;
         }
+        if (p.dk_part) {  // uniform over the grid
+          if (key_ok) {
+            float* part = (w ? p.dv_part : p.dk_part) +
+                          ((static_cast<size_t>(I.b) * p.N + key) * p.Hv + I.hv) * D + 32 * cc;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) st_global_v4(part + 4 * u, a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
+          }
+          continue;
+        }
         uint32_t wv[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -655,7 +672,7 @@ __global__ void __launch_bounds__(512, 1)
       ModBwdItem I;
       mod_bwd_item(p, item, I);
       {
-        int h = I.hk * p.G, i = 0;
+        int h = I.hv * p.hs, i = 0;
         for (int it = 0; it < I.niter; ++it) {
           const uint32_t par = (gt0 + it) & 1;
           const int q = 128 * (I.i_begin + i) + t;
@@ -711,6 +728,29 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+}
+
+// dK = scale * sum, dV = sum of the group's partial sums, in the order of the
+// heads.  One thread per four columns; blockIdx.y: keys or values.
+__global__ void __launch_bounds__(256) fa_mod_bwd_reduce_kernel(const ModBwdParams p, int D) {
+  const int64_t n4 = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const int parts = p.Hv / p.Hkv, q = D / 4;
+  const int64_t row = i / q;  // (token, key head); its partials are rows row * parts ..
+  const float4* src = reinterpret_cast<const float4*>(blockIdx.y ? p.dv_part : p.dk_part) + row * parts * q + i % q;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float4 v = __ldcs(src + static_cast<int64_t>(k) * q);
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  const float mul = blockIdx.y ? 1.f : p.scale;
+  reinterpret_cast<uint2*>(blockIdx.y ? p.dv : p.dk)[i] =
+      make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
 }
 
 }  // namespace fa

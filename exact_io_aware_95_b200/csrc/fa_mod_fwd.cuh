@@ -96,13 +96,15 @@ __device__ __forceinline__ void mod_fwd_item(const ModFwdParams& p, int c, ModFw
   const PlanQTile* qt = p.plan.qt + static_cast<size_t>(it.b) * p.T + 2 * pair;
   const int2 r0 = *reinterpret_cast<const int2*>(qt);  // kbeg, kend
   const int2 r1 = 2 * pair + 1 < p.T ? *reinterpret_cast<const int2*>(qt + 1) : make_int2(0, 0);
-  it.lo0 = r0.x;
-  it.hi0 = r0.y;
-  it.lo1 = r1.x;
-  it.hi1 = r1.y;
-  const bool a0 = r0.x < r0.y, a1 = r1.x < r1.y;
-  it.jb = a0 ? (a1 ? min(r0.x, r1.x) : r0.x) : (a1 ? r1.x : 0);
-  it.je = max(a0 ? r0.y : 0, a1 ? r1.y : 0);
+  // clamped, so that a plan buffer that was never filled gives wrong numbers but
+  // no access outside the tensors
+  it.lo0 = max(r0.x, 0);
+  it.hi0 = min(r0.y, p.T);
+  it.lo1 = max(r1.x, 0);
+  it.hi1 = min(r1.y, p.T);
+  const bool a0 = it.lo0 < it.hi0, a1 = it.lo1 < it.hi1;
+  it.jb = a0 ? (a1 ? min(it.lo0, it.lo1) : it.lo0) : (a1 ? it.lo1 : 0);
+  it.je = max(a0 ? it.hi0 : 0, a1 ? it.hi1 : 0);
 }
 
 template <int D, bool CAP, bool BIAS>

@@ -126,8 +126,8 @@ def mod_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskPlan, s
     return (o, l) if ol is None else (o, l, ol)
 
 
-def mod_bwd_workspace_size(B: int, N: int, H: int, d: int) -> int:
-    return int(lib().fa_mod_bwd_workspace_size(B, N, H, d))
+def mod_bwd_workspace_size(B: int, N: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib().fa_mod_bwd_workspace_size(B, N, H, Hkv, d))
 
 
 def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
@@ -141,7 +141,7 @@ def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: O
     for t, n in ((o, "o"), (do, "do")) + (((o_low, "o_low"),) if o_low is not None else ()):
         _need_shape(t, n, torch.bfloat16, q.shape)
     _need_shape(lse, "lse", torch.float32, (B, H, N))
-    need = mod_bwd_workspace_size(B, N, H, d)
+    need = mod_bwd_workspace_size(B, N, H, Hkv, d)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None else workspace
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk

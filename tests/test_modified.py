@@ -267,7 +267,10 @@ def test_library_refuses_bad_arguments():
     assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, float("inf"), 0.0, None) == inv
     assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, 1.0, -1.0, None) == inv
     assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, 1.0, 1e-40, None) == inv  # scale / softcap is infinite
-    ws = L.fa_mod_bwd_workspace_size(1, 8, 2, 64)
+    ws = L.fa_mod_bwd_workspace_size(1, 8, 2, 1, 64)
+    # dQ accumulator, D, and partial dK and dV where the group's heads are split; nothing of them with enough items
+    assert ws == 4096 + 256 + 2 * 4096 and L.fa_mod_bwd_workspace_size(1, 8, 3, 2, 64) == 0
+    assert L.fa_mod_bwd_workspace_size(8, 8192, 2, 1, 64) == L.fa_bwd_workspace_size(8, 8192, 2, 64)
     b = [P] * 4 + [None] + [P] * 6 + [None, P]  # q k v o o_low lse dO dq dk dv plan slopes workspace
     assert L.fa_mod_bwd(*b, ws - 1, 1, 8, 2, 1, 64, 1.0, 0.0, None) == wsp
     assert L.fa_mod_bwd(*at(b, 12, P + 16), ws, 1, 8, 2, 1, 64, 1.0, 0.0, None) == inv
@@ -309,6 +312,16 @@ def test_lengths(N, mask):
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (6, 6), (6, 3), (8, 1), (14, 2)])
 def test_heads(H, Hkv):
     check(make(2, 200, H, Hkv, 128, 11), {"causal": True}, 50.0, slopes_of(H))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N,H,Hkv", [(8, 400, 16, 8), (1, 1300, 16, 4), (2, 140, 12, 1)])
+def test_groups_whole_and_split(B, N, H, Hkv):
+    """A group's heads in one item, in two or four, and each in its own."""
+    ws = fa.mod_bwd_workspace_size(B, N, H, Hkv, 64)
+    plain = fa.workspace_size(B, N, H, 64)
+    assert (ws == plain) == ((B, H) == (8, 16))
+    check(make(B, N, H, Hkv, 64, 19), {"causal": True}, 30.0, slopes_of(H))
 
 
 @pytest.mark.gpu
