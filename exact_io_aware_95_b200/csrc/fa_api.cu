@@ -582,8 +582,15 @@ fa_status dispatch_mod_bwd(int dev, bool cap, bool bias, const CUtensorMap& q, c
 }
 
 // ------------------------------------------------------------- 8-bit cache
-// Tokens per block: about 64 (token, head) rows, at least one token.
-int cache_tokens_per_block(int Hkv) { return Hkv >= 64 ? 1 : 64 / Hkv; }
+// A block's share of (token, head) rows: about 64 rows of whole tokens, or one
+// token's heads 256 at a time (measured on 8 x 2047 x 8 x 128: 32 rows 23.7 us,
+// 64 rows 21.7, 256 rows 24.8).
+template <typename P>
+void cache_chunks(P& p, int Hkv) {
+  p.tb = Hkv >= 64 ? 1 : 64 / Hkv;
+  p.hb = Hkv > 256 ? 256 : Hkv;
+  p.hchunks = (Hkv + p.hb - 1) / p.hb;
+}
 
 fa_status cache_check(int B, int Nk, int Hkv, int d) {
   if (B < 1 || Nk < 1 || Hkv < 1 || B > 65535) return FA_ERR_INVALID_ARG;
@@ -985,8 +992,10 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_c
   p.T = T;
   p.Nk = Nk;
   p.Hkv = Hkv;
-  p.tb = cache_tokens_per_block(Hkv);
-  const dim3 grid((T + p.tb - 1) / p.tb, B, 2);
+  cache_chunks(p, Hkv);
+  const int64_t gx = static_cast<int64_t>((T + p.tb - 1) / p.tb) * p.hchunks;
+  if (gx > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>(gx), B, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   mark_launch(s);
   if (d == 64) fa::fa_cache_append_kernel<64><<<grid, 256, 0, s>>>(p);
@@ -1009,8 +1018,10 @@ fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens
   p.out = out;
   p.Nk = Nk;
   p.Hkv = Hkv;
-  p.tb = cache_tokens_per_block(Hkv);
-  const dim3 grid((Nk + p.tb - 1) / p.tb, B);
+  cache_chunks(p, Hkv);
+  const int64_t gx = static_cast<int64_t>((Nk + p.tb - 1) / p.tb) * p.hchunks;
+  if (gx > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>(gx), B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   mark_launch(s);
   if (d == 64) fa::fa_cache_read_kernel<64><<<grid, 256, 0, s>>>(p);

@@ -134,7 +134,7 @@ def test_library_refuses_bad_arguments():
 # --------------------------------------------------------- GPU: append, read
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,T,Nk,Hkv,d", [(1, 1, 1, 1, 64), (2, 3, 50, 2, 128), (3, 41, 77, 3, 64), (2, 70, 70, 1, 128),
-                                          (1, 5, 9, 100, 64)])
+                                          (1, 5, 9, 100, 64), (2, 2, 3, 600, 64)])
 def test_append_matches_the_oracle_and_touches_nothing_else(B, T, Nk, Hkv, d):
     k, v = rows(B, T, Hkv, d, 1), rows(B, T, Hkv, d, 2)
     k[0, 0, 0] = 0.0                       # a row of zeros
