@@ -58,7 +58,7 @@ def cache_read(cache: torch.Tensor, scale: torch.Tensor, seqlens: Optional[torch
     B, Nk, Hkv, d = cache.shape
     if seqlens is not None:
         _need_shape(seqlens, "seqlens", torch.int32, (B,))
-    o = torch.empty(cache.shape, dtype=torch.bfloat16, device=cache.device) if out is None else out
+    o = cache.new_empty(cache.shape, dtype=torch.bfloat16) if out is None else out
     _need_shape(o, "out", torch.bfloat16, cache.shape)
     _same_device(cache, scale, o, *(() if seqlens is None else (seqlens,)))
     with _on(cache):
@@ -90,14 +90,20 @@ def cache_decode_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         _need_shape(seqlens_k, "seqlens_k", torch.int32, (B,))
     softcap, window = _softcap(softcap), _window(window)
     _slopes(slopes, H)
-    o = torch.empty_like(q) if out is None else out
-    l = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
-    _need_shape(o, "out", torch.bfloat16, q.shape)
-    _need_shape(l, "lse", torch.float32, (B, H, Nq))
     need = cache_decode_workspace_size(B, Nq, Nk, H, Hkv, d)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None else workspace
-    _need_workspace(ws, need)
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, o, l, ws, *[t for t in (seqlens_k, slopes) if t is not None])
+    ts = [q, k_cache, v_cache, k_scale, v_scale]
+    ts += [t for t in (seqlens_k, slopes) if t is not None]
+    for t, name, dtype, shape in ((out, "out", torch.bfloat16, q.shape), (lse, "lse", torch.float32, (B, H, Nq))):
+        if t is not None:
+            _need_shape(t, name, dtype, shape)
+            ts.append(t)
+    if workspace is not None:
+        _need_workspace(workspace, need)
+        ts.append(workspace)
+    _same_device(*ts)
+    o = q.new_empty(q.shape) if out is None else out
+    l = q.new_empty((B, H, Nq), dtype=torch.float32) if lse is None else lse
+    ws = q.new_empty(max(need, 256), dtype=torch.uint8) if workspace is None else workspace
     with _on(q):
         st = lib().fa_cache_decode_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                        v_scale.data_ptr(), o.data_ptr(), l.data_ptr(),

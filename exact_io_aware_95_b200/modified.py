@@ -109,14 +109,18 @@ def mod_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskPlan, s
     B, N, H, Hkv, d = _sizes(q, k, v, plan)
     softcap = _softcap(softcap)
     _slopes(slopes, H)
-    o = torch.empty_like(q) if out is None else out
-    l = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
-    ol = out_low if out_low is not None else (torch.empty_like(q) if low else None)
-    _need_shape(o, "out", torch.bfloat16, q.shape)
-    _need_shape(l, "lse", torch.float32, (B, H, N))
-    if ol is not None:
-        _need_shape(ol, "out_low", torch.bfloat16, q.shape)
-    _same_device(q, k, v, o, l, plan.data, *[t for t in (ol, slopes) if t is not None])
+    ts = [q, k, v, plan.data]
+    if slopes is not None:
+        ts.append(slopes)
+    for t, name, dtype, shape in ((out, "out", torch.bfloat16, q.shape), (lse, "lse", torch.float32, (B, H, N)),
+                                  (out_low, "out_low", torch.bfloat16, q.shape)):
+        if t is not None:
+            _need_shape(t, name, dtype, shape)
+            ts.append(t)
+    _same_device(*ts)
+    o = q.new_empty(q.shape) if out is None else out
+    l = q.new_empty((B, H, N), dtype=torch.float32) if lse is None else lse
+    ol = out_low if out_low is not None else (q.new_empty(q.shape) if low else None)
     with _on(q):
         st = lib().fa_mod_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                               None if ol is None else ol.data_ptr(), l.data_ptr(), plan.data.data_ptr(),
@@ -142,15 +146,20 @@ def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: O
         _need_shape(t, n, torch.bfloat16, q.shape)
     _need_shape(lse, "lse", torch.float32, (B, H, N))
     need = mod_bwd_workspace_size(B, N, H, Hkv, d)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device) if workspace is None else workspace
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    _need_shape(dq, "dq", torch.bfloat16, q.shape)
-    _need_shape(dk, "dk", torch.bfloat16, k.shape)
-    _need_shape(dv, "dv", torch.bfloat16, k.shape)
-    _need_workspace(ws, need)
-    _same_device(q, k, v, o, lse, do, plan.data, ws, dq, dk, dv, *[t for t in (o_low, slopes) if t is not None])
+    ts = [q, k, v, o, lse, do, plan.data]
+    ts += [t for t in (o_low, slopes) if t is not None]
+    for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
+        if t is not None:
+            _need_shape(t, n, torch.bfloat16, like.shape)
+            ts.append(t)
+    if workspace is not None:
+        _need_workspace(workspace, need)
+        ts.append(workspace)
+    _same_device(*ts)
+    ws = q.new_empty(max(need, 256), dtype=torch.uint8) if workspace is None else workspace
+    dq = q.new_empty(q.shape) if dq is None else dq
+    dk = k.new_empty(k.shape) if dk is None else dk
+    dv = k.new_empty(k.shape) if dv is None else dv
     with _on(q):
         st = lib().fa_mod_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                               None if o_low is None else o_low.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
