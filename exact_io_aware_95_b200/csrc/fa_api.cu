@@ -893,8 +893,6 @@ fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void*
   p.G = H / Hkv;
   p.T = (N + 127) / 128;
   p.npairs = (N + 255) / 256;
-  // K and V of one head; the heads of a group share theirs
-  p.group = head_group((static_cast<int64_t>(N) * d * 2 * 2 + p.G - 1) / p.G, static_cast<int64_t>(B) * H);
   p.scale_log2 = scale * kLog2e;
   p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
   p.cap_log2 = softcap * kLog2e;
@@ -951,7 +949,10 @@ fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o,
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.T = (N + 127) / 128;
-  p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.hs, static_cast<int64_t>(B) * p.Hv);  // Q, dO, dQ acc
+  const int64_t pairs = static_cast<int64_t>(B) * p.Hv;
+  if (pairs > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  p.group = static_cast<int>(pairs);
+  if (pairs * p.T > 4096) p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.hs, pairs);  // Q, dO, dQ acc
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.x_mul = softcap > 0.f ? scale / softcap : 0.f;

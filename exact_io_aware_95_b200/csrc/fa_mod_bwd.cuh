@@ -53,7 +53,7 @@ struct ModBwdParams {
   int B, N, H, Hkv, G;
   int Hv, hs;           // items of a key tile in a batch entry, hs = H / Hv query heads each
   int T;                // ceil(N / 128)
-  int group;            // (entry, Hv) pairs per scheduling group
+  int group;            // (entry, heads) pairs per scheduling group
   float scale, scale_log2, x_mul, cap_log2;
 };
 
@@ -122,9 +122,14 @@ struct ModBwdCfg : BwdCfg<D> {
 };
 
 // One work item: (128-key tile j, batch entry, heads of a key head).  They go in
-// groups of p.group, sized on the host so that a group's Q, dO and dQ
-// accumulator rows stay in L2; inside a group early key tiles go first (under
-// a causal mask they meet the most queries).
+// groups of p.group (entry, heads) pairs, inside a group early key tiles first:
+// under a causal mask they meet the most query tiles, and the longest items have
+// to start first for the persistent CTAs to end together.  The host makes the
+// whole batch one group up to 4096 items; with more, the end of the launch
+// weighs little and groups whose Q, dO and dQ rows stay in L2 are faster.
+// Measured, one group against L2-sized ones: 4 x 16(4) x 4096 x 128 (512 items)
+// 1069 us, 1407; 1 x 8(2) x 16384 x 128 (1024) 1911, 2497; 1 x 16 x 16384 x 128
+// (2048) 3375, 3466; 16 x 32 x 2048 x 64 (8192) 1735, 1565.
 struct ModBwdItem {
   int hv, hk, b, k0, i_begin, ni, niter;  // niter = ni query tiles x hs heads
 };
@@ -427,34 +432,30 @@ __global__ void __launch_bounds__(512, 1)
       const int key = k0 + t;
       const bool key_ok = key < p.N;
       // The terms of this warpgroup's query columns, thread t < 64 those of
-      // column 64w + t of the tile starting at q0: -LSE in base 2 with the
-      // query's part of a one-sided bias, D, and the keys of this tile that
-      // the query sees.  Rows past the end get -LSE = -inf, so P is exactly 0.
-      // `side`: how the bias runs over the tile pair: below the diagonal (or
-      // no row sees past itself) +1, above it -1, both sides 0.
-      float lv = 0.f, dv = 0.f, slope = 0.f;
-      uint32_t sv = 0;
-      int side = 1;
-      bool full = true;
+      // column 64w + t of a tile: LSE, D, the keys that the query sees; and the
+      // tile's own.  They are loaded a tile ahead and only touched when that
+      // tile starts: any arithmetic on them here would wait for the loads.
+      float n_lse, n_dv, n_slope = 0.f;
+      int2 n_see;
+      int n_lo, n_hi, n_ahead;
       auto fetch = [&](int h, int q0) {
-        const PlanQTile qt = p.plan.qt[static_cast<size_t>(I.b) * p.T + (q0 >> 7)];
-        full = k0 >= qt.full_lo && k0 + 128 <= qt.full_hi;
+        const PlanQTile* qt = p.plan.qt + static_cast<size_t>(I.b) * p.T + (q0 >> 7);
+        n_lo = qt->full_lo;
+        n_hi = qt->full_hi;
         if constexpr (BIAS) {
-          slope = p.slopes[h] * kLog2e;
-          side = (q0 >= k0 + 127 || !qt.ahead) ? 1 : (q0 + 127 <= k0 ? -1 : 0);
+          n_ahead = qt->ahead;
+          n_slope = p.slopes[h];
         }
         const int q = q0 + 64 * w + t;
-        lv = -INFINITY;
-        dv = 0.f;
-        sv = 0;
         if (t < 64 && q < p.N) {
           const size_t li = (static_cast<size_t>(I.b) * p.H + h) * p.N + q;
-          lv = -p.lse[li] * kLog2e;
-          dv = p.dvec[li];
-          if constexpr (BIAS) lv -= side * slope * static_cast<float>(q - k0);
-          const int2 x = p.plan.rows[static_cast<size_t>(I.b) * p.N + q];
-          const int lo = min(max(x.x - k0, 0), 128), hi = min(max(x.y - k0, 0), 128);
-          sv = lo | (max(hi - lo, 0) << 16);
+          n_lse = p.lse[li];
+          n_dv = p.dvec[li];
+          n_see = p.plan.rows[static_cast<size_t>(I.b) * p.N + q];
+        } else {  // a row past the end: -LSE = -inf, so P is exactly 0
+          n_lse = INFINITY;
+          n_dv = 0.f;
+          n_see = make_int2(0, 0);
         }
       };
       int h = I.hv * p.hs, i = 0;
@@ -463,15 +464,25 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t par = (gt0 + it) & 1;
         const int q0 = 128 * (I.i_begin + i);
         named_bar_sync(1 + w, 128);  // the warpgroup is done with the previous tile's values
+        const bool tile_full = k0 >= n_lo && k0 + 128 <= n_hi;
+        // How the bias runs over the tile pair: below the diagonal (or no row
+        // sees past itself) +1, above it -1, both sides 0
+        int tile_side = 0;
+        float tile_slope = 0.f;
+        if constexpr (BIAS) {
+          tile_side = (q0 >= k0 + 127 || !n_ahead) ? 1 : (q0 + 127 <= k0 ? -1 : 0);
+          tile_slope = n_slope * kLog2e;
+        }
         if (t < 64) {
+          // -LSE in base 2, with the query's part of a one-sided bias
+          float lv = -n_lse * kLog2e;
+          if constexpr (BIAS) lv -= tile_side * tile_slope * static_cast<float>(q0 + 64 * w + t - k0);
           sLSE[64 * w + t] = lv;
-          sDv[64 * w + t] = dv;
-          sSee[64 * w + t] = sv;
+          sDv[64 * w + t] = n_dv;
+          const int lo = min(max(n_see.x - k0, 0), 128), hi = min(max(n_see.y - k0, 0), 128);
+          sSee[64 * w + t] = lo | (max(hi - lo, 0) << 16);
         }
         named_bar_sync(1 + w, 128);
-        const bool tile_full = full;
-        const int tile_side = side;
-        const float tile_slope = slope;
         if (++i == I.ni) {
           i = 0;
           ++h;

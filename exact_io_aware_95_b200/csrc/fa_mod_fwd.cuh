@@ -69,7 +69,7 @@ struct ModFwdParams {
   PlanView plan;
   int B, N, H, G;       // G = H / Hkv query heads per key head
   int T;                // ceil(N / 128)
-  int npairs, group;
+  int npairs;           // ceil(N / 256)
   float scale_log2;     // scale * log2(e)             (no cap)
   float x_mul;          // scale / cap                 (CAP)
   float cap_log2;       // cap * log2(e)               (CAP)
@@ -84,12 +84,12 @@ struct ModFwdItem {
 };
 
 __device__ __forceinline__ void mod_fwd_item(const ModFwdParams& p, int c, ModFwdItem& it) {
+  // late query blocks first over the whole batch (under a causal mask the
+  // longest), heads side by side: the heads of a group share K and V.  L2-sized
+  // groups of heads, as in the plain forward, were equal or up to 5% slower.
   const int nbh = p.B * p.H;
-  const int g = c / (p.group * p.npairs);
-  const int gs = min(p.group, nbh - g * p.group);
-  const int cc = c - g * p.group * p.npairs;
-  const int bh = g * p.group + cc % gs;
-  const int pair = p.npairs - 1 - cc / gs;
+  const int bh = c % nbh;
+  const int pair = p.npairs - 1 - c / nbh;
   it.h = bh % p.H;
   it.b = bh / p.H;
   it.row0 = pair * 256;
