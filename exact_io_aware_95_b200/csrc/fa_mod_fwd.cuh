@@ -19,18 +19,20 @@
 //     and joins the shared stream only inside it: tiles of other documents,
 //     outside the window or above the diagonal are never loaded or multiplied;
 //   - the softmax warps turn a score row into z (base 2) in registers.  tanh is
-//     an odd polynomial x P(x^2) on |x| <= 1.25, fitted by least squares with
-//     reweighting to an absolute error below 3e-7, evaluated on packed fp32
+//     an odd polynomial x P(x^2) on |x| <= 1, fitted by least squares with
+//     reweighting to an absolute error below 1e-7, evaluated on packed fp32
 //     pairs: 9 packed operations per pair of scores on the FMA pipes, where
 //     exp and a reciprocal would put two more operations per score on the MUFU
 //     pipe that the exponentials already fill (16 per clock per SM).  A warp
-//     whose tile has a score beyond 1.25 cap takes the exponential form for
-//     that tile: 1 - 2 / (1 + e^2x);
+//     whose tile has a score beyond the cap takes the exponential form for that
+//     tile: 1 - 2 / (1 + e^2x);
 //   - the distance bias is linear in j on either side of the diagonal, so on a
 //     tile that lies on one side for all rows of a warp (for causal rows: every
-//     tile) it is one packed FMA with a running column term, the row's part
-//     going into the reference maximum; only tiles that straddle the diagonal
-//     with both sides visible take |i - j| element by element.
+//     tile) it is a packed FMA with the running distance i - j, which is exact;
+//     only tiles that straddle the diagonal with both sides visible take |i - j|
+//     element by element.  (A running product slope j with the row's part taken
+//     into the maximum saves one operation per pair, but adds up 64 roundings at
+//     the size of 128 slopes: 1e-6 of the logsumexp.)
 #pragma once
 #include "fa_fwd.cuh"
 #include "fa_plan.cuh"
@@ -39,12 +41,14 @@ namespace fa {
 
 // tanh x = x P(x^2), |x| <= kTanhRange: coefficients of P in increasing order
 // (fitted in float64 on 4001 points by iteratively reweighted least squares;
-// the largest absolute error is 2.9e-7, 4.5e-7 when evaluated in fp32).
-constexpr float kTanhRange = 1.25f;
+// the largest absolute error is 2.0e-8, 9.5e-8 when evaluated in fp32: at a cap
+// of 50 that is 7e-6 in the exponent, below what the logsumexp keeps.  A range
+// of 1.25 with as many terms has 4.5e-7).
+constexpr float kTanhRange = 1.f;
 constexpr int kTanhTerms = 7;
-__device__ constexpr float kTanhP[kTanhTerms] = {0.9999964833259583f,   -0.33324214816093445f,  0.1326480358839035f,
-                                                 -0.05164468660950661f, 0.01763623207807541f,   -0.004325487185269594f,
-                                                 0.0005254821735434234f};
+__device__ constexpr float kTanhP[kTanhTerms] = {0.9999997019767761f,   -0.33332130312919617f, 0.13319583237171173f,
+                                                 -0.05326583608984947f, 0.019973279908299446f, -0.00595127884298563f,
+                                                 0.0009637715993449092f};
 
 // t = tanh of a packed pair x, |x| <= kTanhRange
 __device__ __forceinline__ uint64_t tanh2_poly(uint64_t x) {
@@ -376,19 +380,19 @@ __global__ void __launch_bounds__(384, 1)
         const int kbase = 128 * j;
         // ---- scores to base-2 logits z, in place.  Without cap and bias s
         // stays raw and the scale is applied with the exponent below.
-        float row_add = 0.f;  // the row's part of a one-sided bias
         if constexpr (CAP || BIAS) {
-          float col_slope = 0.f;  // bias per column, one-sided tiles
+          float side_slope = 0.f;  // -slope below the diagonal, +slope above it: times i - j
           bool straddle = false;
           if constexpr (BIAS) {
             const bool below = behind || kbase + 127 <= qi;
             const bool above = kbase >= qi;
             const bool all_below = __all_sync(0xffffffffu, below), all_above = __all_sync(0xffffffffu, above);
             straddle = !(all_below || all_above);
-            // -slope |qi - (kbase + c)| = -slope (qi - kbase) + slope c below the diagonal
-            col_slope = straddle ? 0.f : (all_below ? slope : -slope);
-            row_add = -col_slope * static_cast<float>(qi - kbase);
+            side_slope = straddle ? 0.f : (all_below ? -slope : slope);
           }
+          const float dist0 = static_cast<float>(qi - kbase);
+          uint64_t d2 = f2_pack(dist0, dist0 - 1.f);
+          const uint64_t m2 = f2_pack(-2.f, -2.f), ss2 = f2_pack(side_slope, side_slope);
           if constexpr (CAP) {
             float ax = 0.f;
 #pragma unroll
@@ -398,20 +402,16 @@ __global__ void __launch_bounds__(384, 1)
                 ax = fmax3(ax, fabsf(__uint_as_float(s[cc][i])), fabsf(__uint_as_float(s[cc][i + 1])));
             const uint64_t xm2 = f2_pack(p.x_mul, p.x_mul), cl2 = f2_pack(p.cap_log2, p.cap_log2);
             if (__all_sync(0xffffffffu, ax * fabsf(p.x_mul) <= kTanhRange)) {
-              uint64_t b2 = f2_pack(0.f, col_slope);
-              const uint64_t st2 = f2_pack(2.f * col_slope, 2.f * col_slope);
 #pragma unroll
               for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                   const uint64_t x = fmul2(f2_pack(__uint_as_float(s[cc][i]), __uint_as_float(s[cc][i + 1])), xm2);
                   const uint64_t th = tanh2_poly(x);
-                  uint64_t z;
+                  uint64_t z = fmul2(th, cl2);
                   if constexpr (BIAS) {
-                    z = ffma2(th, cl2, b2);
-                    b2 = fadd2(b2, st2);
-                  } else {
-                    z = fmul2(th, cl2);
+                    z = ffma2(ss2, d2, z);
+                    d2 = fadd2(d2, m2);
                   }
                   float z0, z1;
                   f2_unpack(z, z0, z1);
@@ -419,33 +419,34 @@ __global__ void __launch_bounds__(384, 1)
                   s[cc][i + 1] = __float_as_uint(z1);
                 }
             } else {
-              float bc = 0.f;
+              float dist = dist0;
 #pragma unroll
               for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  s[cc][i] = __float_as_uint(fmaf(tanh_any(__uint_as_float(s[cc][i]) * p.x_mul), p.cap_log2, bc));
-                  if (BIAS) bc += col_slope;
+                  float z = tanh_any(__uint_as_float(s[cc][i]) * p.x_mul) * p.cap_log2;
+                  if (BIAS) z = fmaf(side_slope, dist, z);
+                  dist -= 1.f;
+                  s[cc][i] = __float_as_uint(z);
                 }
             }
           } else {
             const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-            uint64_t b2 = f2_pack(0.f, col_slope);
-            const uint64_t st2 = f2_pack(2.f * col_slope, 2.f * col_slope);
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 float z0, z1;
-                f2_unpack(ffma2(f2_pack(__uint_as_float(s[cc][i]), __uint_as_float(s[cc][i + 1])), c2, b2), z0, z1);
-                b2 = fadd2(b2, st2);
+                const uint64_t y = fmul2(f2_pack(__uint_as_float(s[cc][i]), __uint_as_float(s[cc][i + 1])), c2);
+                f2_unpack(ffma2(ss2, d2, y), z0, z1);
+                d2 = fadd2(d2, m2);
                 s[cc][i] = __float_as_uint(z0);
                 s[cc][i + 1] = __float_as_uint(z1);
               }
           }
           if constexpr (BIAS) {
             if (straddle) {
-              float dist = static_cast<float>(qi - kbase);
+              float dist = dist0;
 #pragma unroll
               for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
@@ -460,10 +461,14 @@ __global__ void __launch_bounds__(384, 1)
         if (kbase < see.x || kbase + 128 > see.y) {
           const int lo = see.x - kbase, hi = see.y - kbase;
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
+          for (int cc = 0; cc < 4; ++cc) {
+            // bits [lo, hi) of the chunk's 32 columns
+            const int l32 = min(max(lo - 32 * cc, 0), 32), h32 = min(max(hi - 32 * cc, 0), 32);
+            const uint32_t seen = (h32 == 32 ? 0xffffffffu : (1u << h32) - 1u) & (l32 == 32 ? 0u : 0xffffffffu << l32);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * cc + i < lo || 32 * cc + i >= hi) s[cc][i] = __float_as_uint(-INFINITY);
+              if (!(seen & (1u << i))) s[cc][i] = __float_as_uint(-INFINITY);
+          }
         }
         // ---- row max: four independent chains of three-input maxima
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int a = 0; a < 4; ++a)
               mx[a] = fmax3(mx[a], __uint_as_float(s[cc][i + 2 * a]), __uint_as_float(s[cc][i + 2 * a + 1]));
         const float mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float mt = (CAP || BIAS) ? mraw + row_add : mraw * p.scale_log2;
+        const float mt = (CAP || BIAS) ? mraw : mraw * p.scale_log2;
         const bool move = (mt > m + kRescaleThreshold) || (m == -INFINITY && mt > -INFINITY);
         float alpha = 1.f;
         if (move) {
@@ -503,7 +508,7 @@ __global__ void __launch_bounds__(384, 1)
             tmem_wait_st();
           }
         }
-        const float neg_m = (m == -INFINITY) ? 0.f : row_add - m;
+        const float neg_m = (m == -INFINITY) ? 0.f : -m;
         const uint64_t nm2 = f2_pack(neg_m, neg_m);
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
 #pragma unroll

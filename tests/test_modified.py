@@ -61,7 +61,7 @@ def plan_of(mask, B, N):
 def bounds(x, see, scale, softcap, slopes):
     """Element bounds of the kernels' error, from their roundings:
 
-    z     fp32 sum of d products (d 2^-24 of sum |q k|), the cap's tanh (4.5e-7
+    z     fp32 sum of d products (d 2^-24 of sum |q k|), the cap's tanh (4.5e-7 at most
           absolute) and a few fp32 operations on |z| and the bias
     O     each weight rounded to bf16 (U, numerator and normaliser: 2 U), the
           error of z in both (2 dz), O rounded to bf16 (U)
