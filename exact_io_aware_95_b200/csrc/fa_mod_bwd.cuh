@@ -29,15 +29,27 @@
 //     k = N(0,1), d = 64, N = 1024;
 //   - the row term of the exponent, -LSE_i log2 e, carries the query's part of
 //     a one-sided distance bias (the key's part is one constant per thread);
-//   - with CAP the thread keeps bf16(P (1 - t^2)) instead of bf16(P) for dS,
-//     so the extra factor costs no registers between the two phases.
+//   - between its two phases the thread keeps P (1 - t^2) 2^15 in fp16 for dS:
+//     one register per pair as with bf16(P), but with an error of 2^-11 instead
+//     of 2^-8 down to P = 2^-29 (below, 2^-40 absolute: less than the rounding
+//     of any row's larger terms), which leaves the rounding of dS to bf16 as the
+//     one that shows (relative error of dQ 2.4e-3, with bf16 there 3.0e-3).
 #pragma once
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "fa_bwd.cuh"
 #include "fa_mod_fwd.cuh"
 
 namespace fa {
+
+constexpr float kDsUp = 32768.f;  // P <= 1 (and a rounding) times this stays finite in fp16
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 struct ModBwdParams {
   const void* o;
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(512, 1)
           float lv = -n_lse * kLog2e;
           if constexpr (BIAS) lv -= tile_side * tile_slope * static_cast<float>(q0 + 64 * w + t - k0);
           sLSE[64 * w + t] = lv;
-          sDv[64 * w + t] = n_dv;
+          sDv[64 * w + t] = -n_dv / kDsUp;
           const int lo = min(max(n_see.x - k0, 0), 128), hi = min(max(n_see.y - k0, 0), 128);
           sSee[64 * w + t] = lo | (max(hi - lo, 0) << 16);
         }
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(512, 1)
         // the key's part of a one-sided bias
         const float kb = BIAS ? tile_side * tile_slope * static_cast<float>(t) : 0.f;
         const uint64_t kb2 = f2_pack(kb, kb);
-        uint32_t pk[2][16];  // bf16 pairs of P, or of P (1 - t^2) with CAP
+        uint32_t pk[2][16];  // fp16 pairs of P (1 - t^2) 2^15
 #pragma unroll
         for (int hc = 0; hc < 2; ++hc) {
           const int cc = 2 * w + hc;  // 32-column chunk of the 128-column tile
@@ -553,14 +565,13 @@ __global__ void __launch_bounds__(512, 1)
               const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
               pw[2 * m] = pack_bf16x2(p0, p1);
               pw[2 * m + 1] = pack_bf16x2(p2, p3);
-              if constexpr (CAP) {  // P (1 - t^2)
-                const uint64_t one = f2_pack(1.f, 1.f), neg = f2_pack(-1.f, -1.f);
-                float a, b;
-                f2_unpack(fmul2(f2_pack(p0, p1), ffma2(fmul2(s01, neg), s01, one)), a, b);
-                pk[hc][2 * m] = pack_bf16x2(a, b);
-                f2_unpack(fmul2(f2_pack(p2, p3), ffma2(fmul2(s23, neg), s23, one)), a, b);
-                pk[hc][2 * m + 1] = pack_bf16x2(a, b);
-              }
+              // P (1 - t^2) 2^15
+              const uint64_t up = f2_pack(kDsUp, kDsUp), down = f2_pack(-kDsUp, -kDsUp);
+              float a, b;
+              f2_unpack(fmul2(f2_pack(p0, p1), CAP ? ffma2(fmul2(s01, down), s01, up) : up), a, b);
+              pk[hc][2 * m] = pack_f16x2(a, b);
+              f2_unpack(fmul2(f2_pack(p2, p3), CAP ? ffma2(fmul2(s23, down), s23, up) : up), a, b);
+              pk[hc][2 * m + 1] = pack_f16x2(a, b);
             }
           };
           if constexpr (BIAS) {
@@ -578,15 +589,9 @@ __global__ void __launch_bounds__(512, 1)
               const uint32_t k23 = (seen(sw.z) ? 0xffffu : 0u) | (seen(sw.w) ? 0xffff0000u : 0u);
               pw[2 * m] &= k01;
               pw[2 * m + 1] &= k23;
-              if constexpr (CAP) {
-                pk[hc][2 * m] &= k01;
-                pk[hc][2 * m + 1] &= k23;
-              }
+              pk[hc][2 * m] &= k01;
+              pk[hc][2 * m + 1] &= k23;
             }
-          }
-          if constexpr (!CAP) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[hc][e] = pw[e];
           }
           // P^T (bf16) into the first half of this warpgroup's own S^T columns
           tmem_st16(lane_base + C::TM_S + 64 * w + 16 * hc, pw);
@@ -615,11 +620,15 @@ __global__ void __launch_bounds__(512, 1)
             const float4 d4 = sDv4[8 * cc + m];
             const uint32_t a0 = pk[hc][2 * m], a1 = pk[hc][2 * m + 1];
             float d0, d1, d2, d3;
-            f2_unpack(fmul2(f2_pack(bf16lo_to_f32(a0), bf16hi_to_f32(a0)),
-                            fsub2(f2_pack(__uint_as_float(dp[4 * m + 0]), __uint_as_float(dp[4 * m + 1])),
+            // (dP - D) 2^-15 times the kept factor: exact scalings
+            const uint64_t dn = f2_pack(1.f / kDsUp, 1.f / kDsUp);
+            const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&a0));
+            const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&a1));
+            f2_unpack(fmul2(f2_pack(g01.x, g01.y),
+                            ffma2(f2_pack(__uint_as_float(dp[4 * m + 0]), __uint_as_float(dp[4 * m + 1])), dn,
                                   f2_pack(d4.x, d4.y))), d0, d1);
-            f2_unpack(fmul2(f2_pack(bf16lo_to_f32(a1), bf16hi_to_f32(a1)),
-                            fsub2(f2_pack(__uint_as_float(dp[4 * m + 2]), __uint_as_float(dp[4 * m + 3])),
+            f2_unpack(fmul2(f2_pack(g23.x, g23.y),
+                            ffma2(f2_pack(__uint_as_float(dp[4 * m + 2]), __uint_as_float(dp[4 * m + 3])), dn,
                                   f2_pack(d4.z, d4.w))), d2, d3);
             wv[2 * m] = pack_bf16x2(d0, d1);
             wv[2 * m + 1] = pack_bf16x2(d2, d3);

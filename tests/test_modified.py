@@ -17,7 +17,8 @@ from exact_io_aware_95_b200 import build as fabuild
 from oracle import modified as om
 from tests.common import f64, rel_fro
 
-U = 2.0 ** -8   # a rounding to bf16 is off by at most this, relative to the value
+U = 2.0 ** -8     # a rounding to bf16 is off by at most this, relative to the value
+H16 = 2.0 ** -11  # a rounding to fp16
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -67,8 +68,9 @@ def bounds(x, see, scale, softcap, slopes):
           error of z in both (2 dz), O rounded to bf16 (U)
     D     O with its residual: the weights' 2 U and 2 dz, residual rounded (U^2)
     dV    P rounded (U), P's own dz, dV rounded (U)
-    dS    P (1 - t^2) rounded (U), rounded again (U), dz in P and in 1 - t^2
-          (its derivative is at most 2 |t| / cap < 2 / cap <= dz-small), D
+    dS    P (1 - t^2) 2^15 rounded to fp16 (2^-11, or half of its smallest step
+          2^-24, which is 2^-40 of P's scale, where that is more), the result to
+          bf16 (U), dz in P and in 1 - t^2 (its derivative is at most 2 / cap), D
     dQ,dK sums of dS, rounded (U)
     fp32 sums over N terms add N 2^-24 of the absolute sums, inside the slack
     of 2^-16 taken on every absolute sum."""
@@ -98,7 +100,8 @@ def bounds(x, see, scale, softcap, slopes):
             dD = (np.abs(gh) * (o_in + U * U * np.abs(O))).sum(1, keepdims=True)
             ddp = d * 2.0 ** -23 * (np.abs(gh) @ np.abs(vh).T)
             df = 2 * dz / softcap if softcap else 0.0
-            e = p * (f * ((2 * U + 2 * dz + slack) * np.abs(dp - D) + (1 + 2 * U) * (dD + ddp)) + df * np.abs(dp - D))
+            e = p * (f * ((U + H16 + 2 * dz + slack) * np.abs(dp - D) + (1 + 2 * U) * (dD + ddp)) + df * np.abs(dp - D))
+            e = e + np.where(see[b], 2.0 ** -40 * (1 + U) * np.abs(dp - D), 0.0)
             ds = np.abs(p * f * (dp - D))
             g = om.mod_head_bwd(qh, kh, vh, gh, see[b], scale, softcap, sl)
             s = abs(scale)
@@ -110,9 +113,9 @@ def bounds(x, see, scale, softcap, slopes):
     return out
 
 
-# Frobenius bar of a gradient: three roundings to bf16 of at most U each stand
-# between the inputs and dQ or dK (P (1 - t^2), dS, the result), two for dV.
-FRO = {"o": 2 * U, "dq": 3 * U, "dk": 3 * U, "dv": 2 * U}
+# Frobenius bar of a gradient: two roundings to bf16 of at most U each (dS, the
+# result) and one to fp16 stand between the inputs and dQ or dK, two for dV.
+FRO = {"o": 2 * U, "dq": 2 * U + H16, "dk": 2 * U + H16, "dv": 2 * U}
 
 
 def check(x, mask, softcap=0.0, slopes=None, low=True):
