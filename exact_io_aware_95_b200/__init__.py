@@ -155,12 +155,18 @@ def _need_workspace(ws, need: int):
 
 def _same_device(*ts):
     """Every tensor on one CUDA device (checked after dtypes and shapes, right
-    before the call)."""
+    before the call); None stands for an optional one that was not given."""
     at = ts[0].get_device()  # -1: not on a GPU
-    if at >= 0 and all([t.get_device() == at for t in ts]):
-        return
+    if at >= 0:
+        for t in ts:
+            if t is not None and t.get_device() != at:
+                break
+        else:
+            return
     dev = ts[0].device
     for t in ts:
+        if t is None:
+            continue
         if not t.is_cuda:
             raise ValueError(f"all tensors must be on a CUDA device; got one on {t.device}")
         if t.device != dev:

@@ -42,7 +42,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     _need_shape(start, "start", torch.int32, (B,))
     if count is not None:
         _need_shape(count, "count", torch.int32, (B,))
-    _same_device(k, v, k_cache, v_cache, k_scale, v_scale, start, *(() if count is None else (count,)))
+    _same_device(k, v, k_cache, v_cache, k_scale, v_scale, start, count)
     with _on(k):
         st = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                    k_scale.data_ptr(), v_scale.data_ptr(), start.data_ptr(),
@@ -60,7 +60,7 @@ def cache_read(cache: torch.Tensor, scale: torch.Tensor, seqlens: Optional[torch
         _need_shape(seqlens, "seqlens", torch.int32, (B,))
     o = cache.new_empty(cache.shape, dtype=torch.bfloat16) if out is None else out
     _need_shape(o, "out", torch.bfloat16, cache.shape)
-    _same_device(cache, scale, o, *(() if seqlens is None else (seqlens,)))
+    _same_device(cache, scale, o, seqlens)
     with _on(cache):
         st = lib().fa_cache_read(cache.data_ptr(), scale.data_ptr(), None if seqlens is None else seqlens.data_ptr(),
                                  o.data_ptr(), B, Nk, Hkv, d, _stream_ptr(cache))
@@ -90,26 +90,24 @@ def cache_decode_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         _need_shape(seqlens_k, "seqlens_k", torch.int32, (B,))
     softcap, window = _softcap(softcap), _window(window)
     _slopes(slopes, H)
-    need = cache_decode_workspace_size(B, Nq, Nk, H, Hkv, d)
-    ts = [q, k_cache, v_cache, k_scale, v_scale]
-    ts += [t for t in (seqlens_k, slopes) if t is not None]
-    for t, name, dtype, shape in ((out, "out", torch.bfloat16, q.shape), (lse, "lse", torch.float32, (B, H, Nq))):
-        if t is not None:
-            _need_shape(t, name, dtype, shape)
-            ts.append(t)
+    L = lib()
+    need = L.fa_cache_decode_workspace_size(B, Nq, Nk, H, Hkv, d)
+    if out is not None:
+        _need_shape(out, "out", torch.bfloat16, q.shape)
+    if lse is not None:
+        _need_shape(lse, "lse", torch.float32, (B, H, Nq))
     if workspace is not None:
         _need_workspace(workspace, need)
-        ts.append(workspace)
-    _same_device(*ts)
-    o = q.new_empty(q.shape) if out is None else out
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, seqlens_k, slopes, out, lse, workspace)
+    o = torch.empty_like(q) if out is None else out
     l = q.new_empty((B, H, Nq), dtype=torch.float32) if lse is None else lse
     ws = q.new_empty(max(need, 256), dtype=torch.uint8) if workspace is None else workspace
     with _on(q):
-        st = lib().fa_cache_decode_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        st = L.fa_cache_decode_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                        v_scale.data_ptr(), o.data_ptr(), l.data_ptr(),
                                        None if seqlens_k is None else seqlens_k.data_ptr(),
                                        None if slopes is None else slopes.data_ptr(), ws.data_ptr(),
-                                       ws.numel() * ws.element_size(), B, Nq, Nk, H, Hkv, d, _scale(scale, d), softcap,
+                                       ws.nbytes, B, Nq, Nk, H, Hkv, d, _scale(scale, d), softcap,
                                        window, int(bool(causal)), _stream_ptr(q))
     _check(st, "fa_cache_decode_fwd")
     return o, l

@@ -195,6 +195,27 @@ fa_status launch_status(cudaStream_t s) {
   return FA_OK;
 }
 
+// Launch with programmatic stream serialisation: the kernel's blocks may be
+// placed while the kernel before it on the stream ends, and wait for its end
+// (griddepcontrol.wait) before they read.
+template <typename... P, typename... A>
+fa_status launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Heads per scheduling group: as many as keep `bytes_per_head` of streamed
@@ -480,7 +501,9 @@ fa::PlanView plan_view(const void* plan, int B, int N) {
 }
 // Limits shared by the modified-score calls: positions and tile indexes fit
 // 32 bits with room for the window and tile arithmetic.
-bool valid_plan_shape(int B, int N) { return B >= 1 && N >= 1 && N <= (1 << 24); }
+bool valid_plan_shape(int B, int N) {
+  return B >= 1 && B <= 65535 && N >= 1 && N <= (1 << 24) && static_cast<int64_t>(B) * N <= 0x7fffffff;
+}
 
 // ------------------------------------------------- modified-score attention
 fa_status mod_check(int B, int N, int H, int Hkv, int d, float scale, float softcap, const void* plan,
@@ -492,7 +515,6 @@ fa_status mod_check(int B, int N, int H, int Hkv, int d, float scale, float soft
   // scale / softcap and softcap * log2(e) must be representable
   if (softcap > 0.f && (!std::isfinite(scale / softcap) || !std::isfinite(softcap * kLog2e))) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(B) * N > 0x7fffffff) return FA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * N * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
@@ -617,9 +639,6 @@ CacheDecodeWs cache_decode_ws(int Hkv, int d) {
   return w;
 }
 
-// The merge kernel is launched with programmatic stream serialisation: its
-// blocks may be placed while the stream kernel ends, and wait for its end
-// (griddepcontrol) before they read.
 template <int D, int NB, bool CAP, bool BIAS>
 fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap& mv, fa::CDecParams p, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
@@ -639,21 +658,10 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   mark_launch(s);
   kern<<<static_cast<unsigned>(p.groups) * p.Hkv, fa::CDecCfg<D, NB>::THREADS, smem, s>>>(mk, mv, p);
   if ((st = launch_status(s)) != FA_OK) return st;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.by_segment ? segments : p.groups) * p.Hkv, p.rows < p.rpb ? p.rows : p.rpb);
+  const dim3 merge(static_cast<unsigned>(p.by_segment ? segments : p.groups) * p.Hkv, p.rows < p.rpb ? p.rows : p.rpb);
   // records of a segment: about groups / segments.  Few: small blocks, all of them resident at once
-  cfg.blockDim = dim3(segments * 8 < p.groups ? 512 : 128);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_cache_decode_merge_kernel<D>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return FA_ERR_CUDA;
-  }
-  return launch_status(s);
+  st = launch_dependent(fa::fa_cache_decode_merge_kernel<D>, merge, segments * 8 < p.groups ? 512 : 128, s, p);
+  return st != FA_OK ? st : launch_status(s);
 }
 
 template <int D, int NB>
@@ -851,7 +859,6 @@ fa_status fa_mask_plan(void* plan, size_t plan_bytes, const int* doc_ids, const 
   LaunchEventsScope hook_scope;
   if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) != 0) return FA_ERR_INVALID_ARG;
   if (!valid_plan_shape(B, N) || window < 0) return FA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(B) * N > 0x7fffffff) return FA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(doc_ids) & 3u) != 0 || (reinterpret_cast<uintptr_t>(prefix_len) & 3u) != 0)
     return FA_ERR_INVALID_ARG;
@@ -861,9 +868,13 @@ fa_status fa_mask_plan(void* plan, size_t plan_bytes, const int* doc_ids, const 
   if (st != FA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   mark_launch(s);
-  fa::fa_mask_plan_kernel<<<static_cast<unsigned>(B), fa::kPlanThreads, 0, s>>>(plan_view(plan, B, N), doc_ids,
-                                                                                prefix_len, N, window, causal);
-  return launch_status(s);
+  const fa::PlanView pv = plan_view(plan, B, N);
+  const int T = (N + 127) / 128;
+  const dim3 grid((N + fa::kPlanThreads - 1) / fa::kPlanThreads, B);
+  fa::fa_mask_plan_kernel<<<grid, fa::kPlanThreads, 0, s>>>(pv, doc_ids, prefix_len, N, window, causal);
+  if ((st = launch_status(s)) != FA_OK || grid.x == 1) return st;
+  st = launch_dependent(fa::fa_mask_plan_tiles_kernel, dim3((T + 3) / 4, B), 128, s, pv, T);
+  return st != FA_OK ? st : launch_status(s);
 }
 
 fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void* o_low, float* lse, const void* plan,

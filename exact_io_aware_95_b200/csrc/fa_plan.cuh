@@ -12,11 +12,12 @@
 // attention kernels loop over.  The plan depends on the batch alone and is
 // made once for all layers, heads and directions.
 //
-// One block per batch entry.  The runs of equal ids come from two block scans
-// (last start at or before i, first start after i) over per-thread chunks; the
-// tile ranges from warp reductions over 128 rows.  Bound by latency: about
-// 6 us at N = 16384, against hundreds of microseconds for the attention that
-// uses it.
+// One block per 1024 rows, a thread a row.  The run of equal ids around a row
+// comes from a scan over the block; a run that reaches past the block is followed
+// outside it, 4096 ids at a time.  The ranges of query tiles per key tile need
+// the tiles of the whole entry: a second small kernel, or the same block where
+// there is only one.  Bound by latency (one block per entry took 22 us at
+// N = 16384, three per cent of the attention that uses the plan).
 #pragma once
 #include "sm100_ptx.cuh"
 
@@ -44,123 +45,158 @@ struct PlanView {
 
 constexpr int kPlanThreads = 1024;
 
+// Query tiles that meet key tile k: first and last overlap (tiles in between
+// that do not overlap are masked row by row).  A warp per key tile.
+__device__ __forceinline__ void plan_ktile(const PlanView& pv, size_t b, int T, int k) {
+  const PlanQTile* qt = pv.qt + b * T;
+  int q0 = T, q1 = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x & 31; i < T; i += 32) {
+    const int2 r = *reinterpret_cast<const int2*>(qt + i);  // kbeg, kend
+    if (r.x <= k && k < r.y) {
+      q0 = min(q0, i);
+      q1 = i + 1;
+    }
+  }
+  q0 = __reduce_min_sync(0xffffffffu, q0);
+  q1 = __reduce_max_sync(0xffffffffu, q1);
+  if ((threadIdx.x & 31) == 0) {
+    PlanKTile t;
+    t.qbeg = q1 > 0 ? q0 : 0;
+    t.qend = q1;
+    pv.kt[b * T + k] = t;
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
     fa_mask_plan_kernel(PlanView pv, const int* __restrict__ doc_ids, const int* __restrict__ prefix_len, int N,
                         int window, int causal) {
-  __shared__ int s_last[32], s_first[32];
-  const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  __shared__ int s_a[32], s_b[32];
+  __shared__ int s_tile[8][5];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the tile kernel waits for this grid itself
+  const int b = blockIdx.y, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int T = (N + 127) >> 7;
-  int2* rows = pv.rows + static_cast<size_t>(b) * N;
-  const int pre = prefix_len ? min(max(prefix_len[b], 0), N) : 0;
-  auto finish = [&](int i, int lo, int hi) {
-    if (causal) hi = min(hi, max(i + 1, pre));
+  const int base = blockIdx.x * kPlanThreads, end = min(N, base + kPlanThreads);
+  const int i = base + t;  // this thread's row
+  if (t < 8) {
+    s_tile[t][0] = s_tile[t][3] = N;  // min lo, min hi
+    s_tile[t][1] = s_tile[t][2] = s_tile[t][4] = 0;  // max hi, max lo, ahead
+  }
+  int lo = 0, hi = N;
+  bool pad = false;
+  if (doc_ids) {
+    const int* ids = doc_ids + static_cast<size_t>(b) * N;
+    auto is_start = [&](int k) { return k == 0 || ids[k] != ids[k - 1]; };
+    const bool start = i < N && is_start(i);
+    pad = i < N && ids[i] < 0;
+    // last start at or before this row, first start after it, within the block
+    int mx = start ? i : -1, mn = start ? i : N;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, mx, off), y = __shfl_down_sync(0xffffffffu, mn, off);
+      if (lane >= off) mx = max(mx, x);
+      if (lane < 32 - off) mn = min(mn, y);
+    }
+    if (lane == 31) s_a[warp] = mx;
+    if (lane == 0) s_b[warp] = mn;
+    mn = __shfl_down_sync(0xffffffffu, mn, 1);
+    if (lane == 31) mn = N;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) mx = max(mx, s_a[w]);
+    for (int w = warp + 1; w < 32; ++w) mn = min(mn, s_b[w]);
+    __syncthreads();
+    // the start of the run that reaches into the block from before it
+    int before = base;
+    if (!is_start(base)) {  // uniform; base > 0
+      int found = -1;
+      for (int k1 = base; found < 0 && k1 > 0; k1 -= 4 * kPlanThreads) {  // position 0 is a start
+        int f = -1;
+        for (int e = 0; e < 4; ++e) {
+          const int k = k1 - 4 * kPlanThreads + 4 * t + e;
+          if (k >= 0 && k < k1 && is_start(k)) f = k;
+        }
+        f = __reduce_max_sync(0xffffffffu, f);
+        if (lane == 0) s_a[warp] = f;
+        __syncthreads();
+        for (int w = 0; w < 32; ++w) found = max(found, s_a[w]);
+        __syncthreads();
+      }
+      before = found;
+    }
+    // and the first start behind the block
+    int after = N;
+    for (int k0 = end; after == N && k0 < N; k0 += 4 * kPlanThreads) {
+      int f = N;
+      for (int e = 3; e >= 0; --e) {
+        const int k = k0 + 4 * t + e;
+        if (k < N && is_start(k)) f = k;
+      }
+      f = __reduce_min_sync(0xffffffffu, f);
+      if (lane == 0) s_b[warp] = f;
+      __syncthreads();
+      for (int w = 0; w < 32; ++w) after = min(after, s_b[w]);
+      __syncthreads();
+    }
+    lo = mx >= 0 ? mx : before;
+    hi = mn < N ? mn : after;
+  } else {
+    __syncthreads();  // s_tile is set
+  }
+  if (i < N) {
+    if (causal) {
+      const int pre = prefix_len ? min(max(prefix_len[b], 0), N) : 0;
+      hi = min(hi, max(i + 1, pre));
+    }
     if (window > 0) {
       lo = max(lo, i - window + 1);
       hi = min(hi, window < N ? i + window : N);
     }
-    if (lo >= hi) lo = hi = 0;
-    rows[i] = make_int2(lo, hi);
-  };
-  if (!doc_ids) {
-    for (int i = t; i < N; i += kPlanThreads) finish(i, 0, N);
+    if (pad || lo >= hi) lo = hi = 0;
+    pv.rows[static_cast<size_t>(b) * N + i] = make_int2(lo, hi);
   } else {
-    const int* ids = doc_ids + static_cast<size_t>(b) * N;
-    const int per = (N + kPlanThreads - 1) / kPlanThreads;
-    const int i0 = min(N, t * per), i1 = min(N, i0 + per);
-    // this thread's chunk: its last and its first run start
-    int last = -1, first = N;
-    int prev = i0 > 0 && i0 < N ? ids[i0 - 1] : 0;
-    for (int i = i0; i < i1; ++i) {
-      const int id = ids[i];
-      if (i == 0 || id != prev) {
-        last = i;
-        if (first == N) first = i;
-      }
-      prev = id;
-    }
-    // exclusive scans over the threads: maximum of `last` from the left,
-    // minimum of `first` from the right
-    int mx = last, mn = first;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, mx, off), c = __shfl_down_sync(0xffffffffu, mn, off);
-      if (lane >= off) mx = max(mx, a);
-      if (lane < 32 - off) mn = min(mn, c);
-    }
-    if (lane == 31) s_last[warp] = mx;
-    if (lane == 0) s_first[warp] = mn;
-    __syncthreads();
-    int left = __shfl_up_sync(0xffffffffu, mx, 1), right = __shfl_down_sync(0xffffffffu, mn, 1);
-    if (lane == 0) left = -1;
-    if (lane == 31) right = N;
-    for (int w = 0; w < warp; ++w) left = max(left, s_last[w]);
-    for (int w = warp + 1; w < kPlanThreads / 32; ++w) right = min(right, s_first[w]);
-    // walk the chunk backwards for the run ends, run by run
-    int end = right;
-    for (int i = i1; i > i0;) {
-      // the run that holds row i - 1 inside this chunk starts at s
-      int s = i - 1;
-      while (s > i0 && ids[s - 1] == ids[s]) --s;
-      int lo = s;
-      if (s == i0 && !(i0 == 0 || ids[i0 - 1] != ids[i0])) lo = left;  // it began before the chunk
-      const bool pad = ids[s] < 0;
-      for (int r = s; r < i; ++r) {
-        if (pad) rows[r] = make_int2(0, 0);
-        else finish(r, lo, end);
-      }
-      end = s;
-      i = s;
-    }
+    lo = hi = 0;
   }
-  __syncthreads();  // the block's rows are visible to the block
-  // tile ranges: one warp per query tile
-  PlanQTile* qt = pv.qt + static_cast<size_t>(b) * T;
-  for (int k = warp; k < T; k += kPlanThreads / 32) {
-    int lo_min = N, hi_max = 0, lo_max = 0, hi_min = N, ahead = 0;
-    for (int r = lane; r < 128; r += 32) {
-      const int i = 128 * k + r;
-      if (i < N) {
-        const int2 x = rows[i];
-        lo_max = max(lo_max, x.x);
-        hi_min = min(hi_min, x.y);
-        if (x.x < x.y) {
-          lo_min = min(lo_min, x.x);
-          hi_max = max(hi_max, x.y);
-          ahead |= x.y > i + 1;
-        }
-      }
-    }
-    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
-    hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-    hi_min = __reduce_min_sync(0xffffffffu, hi_min);
-    ahead = __any_sync(0xffffffffu, ahead);
+  // tile ranges: a warp's rows lie in one tile
+  {
+    const bool in = i < N, some = in && lo < hi;
+    const int lo_min = __reduce_min_sync(0xffffffffu, some ? lo : N);
+    const int hi_max = __reduce_max_sync(0xffffffffu, some ? hi : 0);
+    const int lo_max = __reduce_max_sync(0xffffffffu, in ? lo : 0);
+    const int hi_min = __reduce_min_sync(0xffffffffu, in ? hi : N);
+    const int ahead = __any_sync(0xffffffffu, some && hi > i + 1);
     if (lane == 0) {
-      PlanQTile q;
-      q.kbeg = hi_max > 0 ? lo_min >> 7 : 0;
-      q.kend = hi_max > 0 ? (hi_max + 127) >> 7 : 0;
-      q.full_lo = lo_max;
-      q.full_hi = hi_min;
-      q.ahead = ahead;
-      q.pad[0] = q.pad[1] = q.pad[2] = 0;
-      qt[k] = q;
+      int* x = s_tile[warp >> 2];
+      atomicMin(x + 0, lo_min);
+      atomicMax(x + 1, hi_max);
+      atomicMax(x + 2, lo_max);
+      atomicMin(x + 3, hi_min);
+      atomicOr(x + 4, ahead);
     }
   }
   __syncthreads();
-  // query tiles that meet each key tile: first and last overlap (tiles in
-  // between that do not overlap are masked row by row)
-  PlanKTile* kt = pv.kt + static_cast<size_t>(b) * T;
-  for (int k = t; k < T; k += kPlanThreads) {
-    int q0 = T, q1 = 0;
-    for (int i = 0; i < T; ++i) {
-      if (qt[i].kbeg <= k && k < qt[i].kend) {
-        q0 = min(q0, i);
-        q1 = i + 1;
-      }
-    }
-    kt[k].qbeg = q1 > 0 ? q0 : 0;
-    kt[k].qend = q1;
+  PlanQTile* qt = pv.qt + static_cast<size_t>(b) * T;
+  const int k = blockIdx.x * 8 + t;
+  if (t < 8 && k < T) {
+    const int* x = s_tile[t];
+    PlanQTile q;
+    q.kbeg = x[1] > 0 ? x[0] >> 7 : 0;
+    q.kend = x[1] > 0 ? (x[1] + 127) >> 7 : 0;
+    q.full_lo = x[2];
+    q.full_hi = x[3];
+    q.ahead = x[4];
+    q.pad[0] = q.pad[1] = q.pad[2] = 0;
+    qt[k] = q;
   }
+  if (gridDim.x == 1) {
+    __syncthreads();  // the block's tiles are visible to the block
+    if (warp < T) plan_ktile(pv, b, T, warp);
+  }
+}
+
+__global__ void __launch_bounds__(128) fa_mask_plan_tiles_kernel(PlanView pv, int T) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' kernel has ended and its tiles are visible
+  const int k = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (k < T) plan_ktile(pv, blockIdx.y, T, k);
 }
 
 }  // namespace fa

@@ -61,22 +61,21 @@ def mask_plan(B: int, N: int, causal: bool = False, window: int = 0, doc_ids: Op
     than that.  device: where to make it (that of the tensors given, else the
     current CUDA device)."""
     B, N, window = int(B), int(N), _window(window)
-    given = []
     if doc_ids is not None:
         _need_shape(doc_ids, "doc_ids", torch.int32, (B, N))
-        given.append(doc_ids)
     if prefix is not None:
         _need_shape(prefix, "prefix", torch.int32, (B,))
-        given.append(prefix)
-    need = int(lib().fa_mask_plan_size(B, N))
+    L = lib()
+    need = L.fa_mask_plan_size(B, N)
     if need == 0:
         raise ValueError(f"no mask plan for B = {B}, N = {N}")
     if device is None:
-        device = given[0].device if given else torch.device("cuda", torch.cuda.current_device())
+        like = doc_ids if doc_ids is not None else prefix
+        device = like.device if like is not None else torch.device("cuda", torch.cuda.current_device())
     data = torch.empty(need, dtype=torch.uint8, device=device)
-    _same_device(data, *given)
+    _same_device(data, doc_ids, prefix)
     with _on(data):
-        st = lib().fa_mask_plan(data.data_ptr(), need, None if doc_ids is None else doc_ids.data_ptr(),
+        st = L.fa_mask_plan(data.data_ptr(), need, None if doc_ids is None else doc_ids.data_ptr(),
                                 None if prefix is None else prefix.data_ptr(), B, N, window, int(bool(causal)),
                                 _stream_ptr(data))
     _check(st, "fa_mask_plan")
@@ -88,7 +87,7 @@ def _sizes(q, k, v, plan):
     _need(k, "k", torch.bfloat16, 4)
     B, N, H, d = q.shape
     Hkv = k.shape[2]
-    if tuple(k.shape) != (B, N, Hkv, d) or Hkv < 1 or H % Hkv != 0:
+    if k.shape != (B, N, Hkv, d) or Hkv < 1 or H % Hkv != 0:
         raise ValueError(f"k must be [{B}, {N}, Hkv, {d}] with Hkv dividing {H}, got {tuple(k.shape)}")
     _need_shape(v, "v", torch.bfloat16, k.shape)
     if not isinstance(plan, MaskPlan):
@@ -109,18 +108,16 @@ def mod_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskPlan, s
     B, N, H, Hkv, d = _sizes(q, k, v, plan)
     softcap = _softcap(softcap)
     _slopes(slopes, H)
-    ts = [q, k, v, plan.data]
-    if slopes is not None:
-        ts.append(slopes)
-    for t, name, dtype, shape in ((out, "out", torch.bfloat16, q.shape), (lse, "lse", torch.float32, (B, H, N)),
-                                  (out_low, "out_low", torch.bfloat16, q.shape)):
-        if t is not None:
-            _need_shape(t, name, dtype, shape)
-            ts.append(t)
-    _same_device(*ts)
-    o = q.new_empty(q.shape) if out is None else out
+    if out is not None:
+        _need_shape(out, "out", torch.bfloat16, q.shape)
+    if lse is not None:
+        _need_shape(lse, "lse", torch.float32, (B, H, N))
+    if out_low is not None:
+        _need_shape(out_low, "out_low", torch.bfloat16, q.shape)
+    _same_device(q, k, v, plan.data, slopes, out, lse, out_low)
+    o = torch.empty_like(q) if out is None else out
     l = q.new_empty((B, H, N), dtype=torch.float32) if lse is None else lse
-    ol = out_low if out_low is not None else (q.new_empty(q.shape) if low else None)
+    ol = out_low if out_low is not None else (torch.empty_like(q) if low else None)
     with _on(q):
         st = lib().fa_mod_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                               None if ol is None else ol.data_ptr(), l.data_ptr(), plan.data.data_ptr(),
@@ -142,31 +139,32 @@ def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: O
     B, N, H, Hkv, d = _sizes(q, k, v, plan)
     softcap = _softcap(softcap)
     _slopes(slopes, H)
-    for t, n in ((o, "o"), (do, "do")) + (((o_low, "o_low"),) if o_low is not None else ()):
-        _need_shape(t, n, torch.bfloat16, q.shape)
+    _need_shape(o, "o", torch.bfloat16, q.shape)
+    _need_shape(do, "do", torch.bfloat16, q.shape)
+    if o_low is not None:
+        _need_shape(o_low, "o_low", torch.bfloat16, q.shape)
     _need_shape(lse, "lse", torch.float32, (B, H, N))
-    need = mod_bwd_workspace_size(B, N, H, Hkv, d)
-    ts = [q, k, v, o, lse, do, plan.data]
-    ts += [t for t in (o_low, slopes) if t is not None]
-    for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
-        if t is not None:
-            _need_shape(t, n, torch.bfloat16, like.shape)
-            ts.append(t)
+    if dq is not None:
+        _need_shape(dq, "dq", torch.bfloat16, q.shape)
+    if dk is not None:
+        _need_shape(dk, "dk", torch.bfloat16, k.shape)
+    if dv is not None:
+        _need_shape(dv, "dv", torch.bfloat16, k.shape)
+    L = lib()
+    need = L.fa_mod_bwd_workspace_size(B, N, H, Hkv, d)
     if workspace is not None:
         _need_workspace(workspace, need)
-        ts.append(workspace)
-    _same_device(*ts)
+    _same_device(q, k, v, o, lse, do, plan.data, o_low, slopes, workspace, dq, dk, dv)
     ws = q.new_empty(max(need, 256), dtype=torch.uint8) if workspace is None else workspace
-    dq = q.new_empty(q.shape) if dq is None else dq
-    dk = k.new_empty(k.shape) if dk is None else dk
-    dv = k.new_empty(k.shape) if dv is None else dv
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(k) if dv is None else dv
     with _on(q):
-        st = lib().fa_mod_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                              None if o_low is None else o_low.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
-                              dk.data_ptr(), dv.data_ptr(), plan.data.data_ptr(),
-                              None if slopes is None else slopes.data_ptr(), ws.data_ptr(),
-                              ws.numel() * ws.element_size(), B, N, H, Hkv, d, _scale(scale, d), softcap,
-                              _stream_ptr(q))
+        st = L.fa_mod_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                          None if o_low is None else o_low.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+                          dk.data_ptr(), dv.data_ptr(), plan.data.data_ptr(),
+                          None if slopes is None else slopes.data_ptr(), ws.data_ptr(), ws.nbytes, B, N, H, Hkv, d,
+                          _scale(scale, d), softcap, _stream_ptr(q))
     _check(st, "fa_mod_bwd")
     return dq, dk, dv
 

@@ -200,8 +200,8 @@ fa_status fa_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
  *   window      > 0: only keys |i - j| < window; 0: no window.
  * `plan` is a device buffer of plan_bytes >= fa_mask_plan_size(B, N) bytes,
  * 256-byte aligned, written on `stream` and read by fa_mod_fwd and fa_mod_bwd
- * for batches of exactly this B and N: make it once per batch.  N <= 2^24,
- * B * N < 2^31.  fa_mask_plan_size returns 0 for invalid sizes. */
+ * for batches of exactly this B and N: make it once per batch.  B <= 65535,
+ * N <= 2^24, B * N < 2^31.  fa_mask_plan_size returns 0 for invalid sizes. */
 size_t fa_mask_plan_size(int B, int N);
 fa_status fa_mask_plan(void* plan, size_t plan_bytes, const int* doc_ids, const int* prefix_len, int B, int N,
                        int window, int causal, void* stream);

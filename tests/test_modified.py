@@ -491,13 +491,14 @@ def test_autograd():
 
 @pytest.mark.gpu
 def test_plan_of_a_long_batch():
-    """Documents over many rows a thread (N above the block's threads), against
-    the definition row by row."""
-    N = 5000
+    """Documents that begin and end in other blocks of rows than theirs, one of
+    them over two whole blocks and more, against the definition row by row."""
+    N = 10300
     g = torch.Generator().manual_seed(26)
     ids = torch.cumsum(torch.rand(2, N, generator=g) < 0.01, 1).int()
-    ids[1, 2500:] = 7
+    ids[1, 1500:9000] = 7
     ids[0, 4000:4100] = -1
+    ids[0, 10250:] = -2
     plan = fa.mask_plan(2, N, causal=True, window=300, doc_ids=ids.cuda(), prefix=torch.tensor([0, 3000], dtype=torch.int32).cuda())
     rows = plan.data[:2 * N * 8].view(torch.int32).view(2, N, 2).cpu()
     for b in range(2):
