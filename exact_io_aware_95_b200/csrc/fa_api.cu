@@ -505,15 +505,24 @@ bool valid_plan_shape(int B, int N) {
   return B >= 1 && B <= 65535 && N >= 1 && N <= (1 << 24) && static_cast<int64_t>(B) * N <= 0x7fffffff;
 }
 
+// Scores: finite scale and cap, and scale / cap and cap * log2(e), by which the
+// kernels multiply, finite and not subnormal.
+bool valid_cap(float scale, float softcap) {
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return false;
+  if (softcap == 0.f) return true;
+  const float x_mul = scale / softcap, cap = softcap * kLog2e;
+  return std::isfinite(x_mul) && std::isfinite(cap) && (scale == 0.f || std::isnormal(x_mul)) && std::isnormal(cap);
+}
+
 // ------------------------------------------------- modified-score attention
 fa_status mod_check(int B, int N, int H, int Hkv, int d, float scale, float softcap, const void* plan,
                     const float* slopes) {
   if (!valid_plan_shape(B, N) || H < 1 || Hkv < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) != 0) return FA_ERR_INVALID_ARG;
   if (slopes && (reinterpret_cast<uintptr_t>(slopes) & 3u) != 0) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return FA_ERR_INVALID_ARG;
-  // scale / softcap and softcap * log2(e) must be representable
-  if (softcap > 0.f && (!std::isfinite(scale / softcap) || !std::isfinite(softcap * kLog2e))) return FA_ERR_INVALID_ARG;
+  // the row maximum is taken of the raw products: a negative scale would turn it into the minimum
+  if (!(scale >= 0.f)) return FA_ERR_INVALID_ARG;
+  if (!valid_cap(scale, softcap)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(B) * N * H * d > (int64_t(1) << 40)) return FA_ERR_INVALID_ARG;
   return FA_OK;
@@ -1060,8 +1069,7 @@ fa_status fa_cache_decode_fwd(const void* q, const void* k_cache, const void* v_
     return FA_ERR_INVALID_ARG;
   if (Nq < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || window < 0) return FA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return FA_ERR_INVALID_ARG;
-  if (softcap > 0.f && (!std::isfinite(scale / softcap) || !std::isfinite(softcap * kLog2e))) return FA_ERR_INVALID_ARG;
+  if (!valid_cap(scale, softcap)) return FA_ERR_INVALID_ARG;
   if (Nq > 16) return FA_ERR_UNSUPPORTED;
   fa_status st = cache_check(B, Nk, Hkv, d);
   if (st != FA_OK) return st;

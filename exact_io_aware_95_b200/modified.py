@@ -12,6 +12,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check, _need, _need_shape, _need_workspace, _on, _same_device, _scale, _stream_ptr, lib
 
@@ -76,8 +77,8 @@ def mask_plan(B: int, N: int, causal: bool = False, window: int = 0, doc_ids: Op
     _same_device(data, doc_ids, prefix)
     with _on(data):
         st = L.fa_mask_plan(data.data_ptr(), need, None if doc_ids is None else doc_ids.data_ptr(),
-                                None if prefix is None else prefix.data_ptr(), B, N, window, int(bool(causal)),
-                                _stream_ptr(data))
+                            None if prefix is None else prefix.data_ptr(), B, N, window, int(bool(causal)),
+                            _stream_ptr(data))
     _check(st, "fa_mask_plan")
     return MaskPlan(data, B, N)
 
@@ -178,6 +179,7 @@ class _ModAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, o_low, data, *slopes = ctx.saved_tensors
         g = mod_bwd(q, k, v, o, lse, do.contiguous(), MaskPlan(data, *ctx.sizes), softcap=ctx.softcap,

@@ -184,6 +184,7 @@ fa_status fa_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
  *   - slopes (fp32 [H] device array, or NULL): the score of query i and key j
  *     is then lowered by slopes[h] * |i - j| (any finite slope);
  *   - the keys each query sees come from a mask plan, not from a flag.
+ * scale is >= 0 here, and scale / softcap a normal number (or 0).
  * A query that sees no key gets O = 0, LSE = -inf and no gradient; a key that
  * no query sees gets dK = dV = 0.  K and V must be finite also in rows that
  * are masked (padding): they enter products with weight 0. */

@@ -291,6 +291,37 @@ def test_decode_splits(B, Nk, Hkv, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,Hkv,Nq", [(1, 600, 1), (3, 500, 3), (1, 149, 9)])
+def test_decode_many_key_heads(B, Hkv, Nq):
+    """More key heads than a wave of thread blocks, and counts that leave part of one unused."""
+    check_decode(query(B, Nq, Hkv, 64, 31), filled(B, 90, Hkv, 64, 32), torch.tensor([90, 0, 33][:B], dtype=torch.int32))
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """Caches of more than 2^31 bytes: rows appended, read and attended to at their end."""
+    B, Nk, Hkv, d, T, W = 2, 600000, 16, 128, 40, 30
+    assert Nk * Hkv * d * B > 2**31
+    c = empty_cache(B, Nk, Hkv, d, fill=0x7f)  # NaN wherever nothing was written
+    k, v = rows(B, T, Hkv, d, 33, 0.3).cuda(), rows(B, T, Hkv, d, 34, 0.3).cuda()
+    start = torch.tensor([Nk - T, Nk - T - 5], dtype=torch.int32).cuda()
+    fa.cache_append(k, v, c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"], start)
+    lens = start + T
+    q = query(B, 2, 32, d, 35)
+    o, lse = fa.cache_decode_fwd(q.cuda(), c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"], lens, causal=True, window=W)
+    fa.check_device_error()
+    small = empty_cache(B, T, Hkv, d)
+    fa.cache_append(k, v, small["k_cache"], small["v_cache"], small["k_scale"], small["v_scale"], torch.zeros_like(start))
+    want = fa.cache_decode_fwd(q.cuda(), small["k_cache"], small["v_cache"], small["k_scale"], small["v_scale"], None, causal=True, window=W)
+    check_decode(q, small, torch.tensor([T, T], dtype=torch.int32), True, window=W)
+    # the same keys at other places of a tile: the sums are taken in another order
+    assert (lse - want[1]).abs().max() <= 1e-5
+    assert ((o - want[0]).float().abs() <= 2 * U * want[0].float().abs() + 2.0 ** -10).all()
+    out = fa.cache_read(c["k_cache"][1:], c["k_scale"][1:], lens[1:])
+    assert torch.equal(out[0, Nk - T - 5:Nk - 5], fa.cache_read(small["k_cache"], small["k_scale"])[1]) and (out[0, Nk - 5:] == 0).all()
+
+
+@pytest.mark.gpu
 def test_decode_spread_of_value_scales():
     """Value rows whose scales differ by tens of powers of two, zero rows, and the
     largest weight on a small row: the output keeps the precision of what it sums."""

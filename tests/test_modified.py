@@ -270,6 +270,9 @@ def test_library_refuses_bad_arguments():
     assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, float("inf"), 0.0, None) == inv
     assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, 1.0, -1.0, None) == inv
     assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, 1.0, 1e-40, None) == inv  # scale / softcap is infinite
+    assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, 1.0, 2e38, None) == inv   # and here subnormal
+    assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, -1.0, 0.0, None) == inv
+    assert L.fa_mod_fwd(*f, 65536, 8, 2, 1, 64, 1.0, 0.0, None) == inv
     ws = L.fa_mod_bwd_workspace_size(1, 8, 2, 1, 64)
     # dQ accumulator, D, and partial dK and dV where the group's heads are split; nothing of them with enough items
     assert ws == 4096 + 256 + 2 * 4096 and L.fa_mod_bwd_workspace_size(1, 8, 3, 2, 64) == 0
@@ -487,6 +490,71 @@ def test_autograd():
         assert torch.equal(fa.mod_attention(q, k, v, plan, softcap=30.0, slopes=sl), o)
     assert torch.equal(o, o1)
     assert torch.equal(k.grad, g[1]) and torch.equal(v.grad, g[2]) and rel_fro(f64(q.grad), f64(g[0])) <= U
+
+
+@pytest.mark.gpu
+def test_autograd_refuses_a_second_derivative():
+    x = make(1, 40, 2, 1, 64, 27)
+    q, k, v = (x[n].cuda().requires_grad_(True) for n in ("q", "k", "v"))
+    o = fa.mod_attention(q, k, v, fa.mask_plan(1, 40, device="cuda"))
+    (g,) = torch.autograd.grad(o, q, x["do"].cuda(), create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.float().sum().backward()
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once_and_from_a_new_host_thread():
+    import threading
+    x = {n: t.cuda() for n, t in make(2, 500, 4, 2, 64, 28).items()}
+    plan = fa.mask_plan(2, 500, causal=True, device="cuda")
+
+    def step():
+        o, lse, low = fa.mod_fwd(x["q"], x["k"], x["v"], plan, softcap=20.0, low=True)
+        return (o, lse) + fa.mod_bwd(x["q"], x["k"], x["v"], o, lse, x["do"], plan, softcap=20.0, o_low=low)
+
+    want = step()
+    torch.cuda.synchronize()
+    got = {}
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(4):
+                got[i] = step()
+            torch.cuda.current_stream().synchronize()
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert len(got) == 3
+    for g in got.values():
+        assert all(torch.equal(g[i], want[i]) for i in (0, 1, 3, 4)) and rel_fro(f64(g[2]), f64(want[2])) <= U
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 elements: the last rows of a windowed batch
+    against the oracle on those rows alone."""
+    N, H, Hkv, d, W, S = 140000, 128, 2, 128, 50, 300
+    assert N * H * d > 2**31
+    g = torch.Generator(device="cuda").manual_seed(29)
+    rand = lambda h: torch.randn(1, N, h, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    q, k, v, do = rand(H), rand(Hkv), rand(Hkv), rand(H)
+    plan = fa.mask_plan(1, N, causal=True, window=W, device="cuda")
+    o, lse, low = fa.mod_fwd(q, k, v, plan, softcap=30.0, low=True)
+    dq, dk, dv = fa.mod_bwd(q, k, v, o, lse, do, plan, softcap=30.0, o_low=low)
+    fa.check_device_error()
+    x = {"q": q[:, -S:, -64:], "k": k[:, -S:, 1:], "v": v[:, -S:, 1:], "do": do[:, -S:, -64:]}  # the last key head's group
+    x = {n: t.cpu() for n, t in x.items()}
+    see = see_of({"causal": True, "window": W}, 1, S)
+    want = dict(zip(("dq", "dk", "dv"), om.mod_attn_bwd(*(f64(x[n]) for n in ("q", "k", "v", "do")), see, 1 / math.sqrt(d), 30.0)))
+    want["o"], _ = om.mod_attn_fwd(*(f64(x[n]) for n in ("q", "k", "v")), see, 1 / math.sqrt(d), 30.0)
+    tol = bounds(x, see, 1 / math.sqrt(d), 30.0, None)
+    got = {"o": o[:, -S:, -64:], "dq": dq[:, -S:, -64:], "dk": dk[:, -S:, 1:], "dv": dv[:, -S:, 1:]}
+    for n, t in got.items():  # rows whose whole window lies in the slice
+        e = np.abs(f64(t) - want[n])[:, W:] - tol[n][:, W:]
+        assert e.max() <= 0, (n, e.max())
 
 
 @pytest.mark.gpu
