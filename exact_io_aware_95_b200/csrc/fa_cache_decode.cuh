@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           for (int c = 0; c < 4; ++c) {
             const int x = 2 * nb + (c & 1), key = k0 + g + 8 * (c >> 1);
             float z = sc[nb][c] * (rowf[x] * ks[c >> 1]);
-            if (CAP) z = p.cap_log2 * tanh_any(z);
+            if (CAP) z = p.cap_log2 * tanh_any(z * kTwoLog2e);
             if (BIAS) z = fmaf(-slope[x], fabsf(static_cast<float>(pos[x] - key)), z);
             float zo = z + ev[c >> 1];
             if (!all_see) {

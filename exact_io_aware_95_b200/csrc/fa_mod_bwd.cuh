@@ -535,8 +535,16 @@ __global__ void __launch_bounds__(512, 1)
                 s[e + 1] = __float_as_uint(b);
               }
             } else {
+              const float xe = p.x_mul * kTwoLog2e;
+              const uint64_t xe2 = f2_pack(xe, xe);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(tanh_any(__uint_as_float(s[e]) * p.x_mul));
+              for (int e = 0; e < 32; e += 2) {
+                float a, b;
+                f2_unpack(tanh2_any(fmul2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), xe2),
+                                    f2_pack(1.f, 1.f), f2_pack(-2.f, -2.f)), a, b);
+                s[e] = __float_as_uint(a);
+                s[e + 1] = __float_as_uint(b);
+              }
             }
           }
           // Everything that depends on the tile is decided outside the column

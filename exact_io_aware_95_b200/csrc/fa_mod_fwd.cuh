@@ -58,11 +58,21 @@ __device__ __forceinline__ uint64_t tanh2_poly(uint64_t x) {
   for (int k = kTanhTerms - 2; k >= 0; --k) r = ffma2(r, u, f2_pack(kTanhP[k], kTanhP[k]));
   return fmul2(r, x);
 }
-// tanh for any x (NaN stays NaN): 1 - 2 / (1 + e^2x); 2 / inf = 0 and e^-inf = 0
-// give the limits
-__device__ __forceinline__ float tanh_any(float x) {
-  const float e = ex2(x * 2.885390081777926815f);
-  return 1.f - __fdividef(2.f, 1.f + e);
+// tanh for any x (NaN stays NaN): 1 - 2 / (1 + e^2x); 1 / inf = 0 and e^-inf = 0
+// give the limits.  The argument is x * 2 log2(e).
+constexpr float kTwoLog2e = 2.885390081777926815f;
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float tanh_any(float x2) { return fmaf(-2.f, rcp_approx(1.f + ex2(x2)), 1.f); }
+// base + mul / (1 + 2^x2) of a packed pair: with (1, -2) the tanh
+__device__ __forceinline__ uint64_t tanh2_any(uint64_t x2, uint64_t base, uint64_t mul) {
+  float a, b;
+  f2_unpack(x2, a, b);
+  f2_unpack(fadd2(f2_pack(ex2(a), ex2(b)), f2_pack(1.f, 1.f)), a, b);
+  return ffma2(f2_pack(rcp_approx(a), rcp_approx(b)), mul, base);
 }
 
 struct ModFwdParams {
@@ -419,15 +429,22 @@ __global__ void __launch_bounds__(384, 1)
                   s[cc][i + 1] = __float_as_uint(z1);
                 }
             } else {
-              float dist = dist0;
+              const float xe = p.x_mul * kTwoLog2e;
+              const uint64_t xe2 = f2_pack(xe, xe), cm2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
 #pragma unroll
               for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  float z = tanh_any(__uint_as_float(s[cc][i]) * p.x_mul) * p.cap_log2;
-                  if (BIAS) z = fmaf(side_slope, dist, z);
-                  dist -= 1.f;
-                  s[cc][i] = __float_as_uint(z);
+                for (int i = 0; i < 32; i += 2) {
+                  uint64_t z = tanh2_any(fmul2(f2_pack(__uint_as_float(s[cc][i]), __uint_as_float(s[cc][i + 1])), xe2),
+                                         cl2, cm2);
+                  if constexpr (BIAS) {
+                    z = ffma2(ss2, d2, z);
+                    d2 = fadd2(d2, m2);
+                  }
+                  float z0, z1;
+                  f2_unpack(z, z0, z1);
+                  s[cc][i] = __float_as_uint(z0);
+                  s[cc][i + 1] = __float_as_uint(z1);
                 }
             }
           } else {
