@@ -46,6 +46,12 @@
 // any arithmetic streamed at 4.2 TB/s.  Partial records of shared segments are
 // merged through their logsumexps by a second kernel.  Each CTA finds its chunk
 // by scanning the lengths itself: no prefix launch.
+//
+// Measured: 16 x 16(16) x 16384 x 128 full 176-190 us (1.08 GB: 0.87-0.94 of the
+// copy bandwidth), 64 x 32(8) x 8192 x 128 ragged and capped 107 us (0.54 GB: 0.77;
+// the rest is the start, the piece ends and the merge), one 100-row cache 7 us,
+// which is the latency of two launches.  ncu: DRAM bytes equal the algorithmic
+// ones, issue slots 50% busy, tensor pipe 17%.
 #pragma once
 #include "fa_cache.cuh"
 #include "fa_mod_fwd.cuh"

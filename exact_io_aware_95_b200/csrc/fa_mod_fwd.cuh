@@ -33,6 +33,15 @@
 //     element by element.  (A running product slope j with the row's part taken
 //     into the maximum saves one operation per pair, but adds up 64 roundings at
 //     the size of 128 slopes: 1e-6 of the logsumexp.)
+// What bounds it is the chain of a score tile through one softmax warpgroup
+// (load, tanh, maximum, exponentials, store), of which two run side by side: at
+// 4 x 16(4) x 4096 x 128 causal, ncu sees 42% of the issue slots, 26% of the
+// tensor pipe, 26% of MUFU and 24% of the FMA pipes busy.  That size takes 300 us
+// with neither cap nor bias (275 GFLOP: 916 TFLOP/s), 367 us with the bias,
+// 475 us with the cap.  Measured and not kept: the score row transformed in
+// rolled 32-column steps through tensor memory (470 us capped, but 727 against
+// 687 us biased at 16384 tokens); the maximum taken of the raw scores and tanh
+// and exponential in one loop (509 against 493 us).
 #pragma once
 #include "fa_fwd.cuh"
 #include "fa_plan.cuh"
