@@ -18,12 +18,12 @@ from .modified import _slopes, _softcap, _window
 __all__ = ["cache_append", "cache_read", "cache_decode_fwd", "cache_decode_workspace_size"]
 
 
-def _need_cache(codes, exps, name: str, shape=None):
-    _need(codes, name + "_cache", torch.float8_e4m3fn, 4)
-    if shape is not None and tuple(codes.shape) != tuple(shape):
-        raise ValueError(f"{name}_cache must have shape {tuple(shape)}, got {tuple(codes.shape)}")
+def _need_cache(codes, exps, name: str, scale_name: str, shape=None):
+    _need(codes, name, torch.float8_e4m3fn, 4)
+    if shape is not None and codes.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(codes.shape)}")
     B, Nk, Hkv, _ = codes.shape
-    _need_shape(exps, name + "_scale", torch.uint8, (B, Hkv, Nk))
+    _need_shape(exps, scale_name, torch.uint8, (B, Hkv, Nk))
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -37,8 +37,8 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     B, T, Hkv, d = k.shape
     _need(k_cache, "k_cache", torch.float8_e4m3fn, 4)
     Nk = k_cache.shape[1]
-    _need_cache(k_cache, k_scale, "k", (B, Nk, Hkv, d))
-    _need_cache(v_cache, v_scale, "v", (B, Nk, Hkv, d))
+    _need_cache(k_cache, k_scale, "k_cache", "k_scale", (B, Nk, Hkv, d))
+    _need_cache(v_cache, v_scale, "v_cache", "v_scale", (B, Nk, Hkv, d))
     _need_shape(start, "start", torch.int32, (B,))
     if count is not None:
         _need_shape(count, "count", torch.int32, (B,))
@@ -54,7 +54,7 @@ def cache_read(cache: torch.Tensor, scale: torch.Tensor, seqlens: Optional[torch
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The cached values as bf16 [B, Nk, Hkv, d], exactly; zero in the rows from
     seqlens[b] (int32 [B]; None: all Nk rows are read) on."""
-    _need_cache(cache, scale, "k")
+    _need_cache(cache, scale, "cache", "scale")
     B, Nk, Hkv, d = cache.shape
     if seqlens is not None:
         _need_shape(seqlens, "seqlens", torch.int32, (B,))
@@ -81,11 +81,11 @@ def cache_decode_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     O bf16 [B, Nq, H, d] and LSE fp32 [B, H, Nq]."""
     _need(q, "q", torch.bfloat16, 4)
     B, Nq, H, d = q.shape
-    _need_cache(k_cache, k_scale, "k")
+    _need_cache(k_cache, k_scale, "k_cache", "k_scale")
     Nk, Hkv = k_cache.shape[1], k_cache.shape[2]
-    if tuple(k_cache.shape) != (B, Nk, Hkv, d) or Hkv < 1 or H % Hkv != 0:
+    if k_cache.shape != (B, Nk, Hkv, d) or Hkv < 1 or H % Hkv != 0:
         raise ValueError(f"k_cache must be [{B}, Nk, Hkv, {d}] with Hkv dividing {H}, got {tuple(k_cache.shape)}")
-    _need_cache(v_cache, v_scale, "v", k_cache.shape)
+    _need_cache(v_cache, v_scale, "v_cache", "v_scale", k_cache.shape)
     if seqlens_k is not None:
         _need_shape(seqlens_k, "seqlens_k", torch.int32, (B,))
     softcap, window = _softcap(softcap), _window(window)

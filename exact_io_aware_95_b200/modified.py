@@ -193,6 +193,6 @@ def mod_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskP
     [B, N, Hkv, d] keys and values; differentiable in q, k, v."""
     if isinstance(q, torch.Tensor) and q.dim() == 4:
         _slopes(slopes, q.shape[2])  # inside a Function no tensor asks for a gradient
-    if not (torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))):
+    if not (torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (q, k, v))):
         return mod_fwd(q, k, v, plan, softcap=softcap, slopes=slopes, scale=scale)[0]
     return _ModAttention.apply(q, k, v, plan, softcap, slopes, scale)
