@@ -460,13 +460,50 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
         const bool all_see = k0 >= full_lo && k0 + 16 <= full_hi;  // warp-uniform
         float so[NB][4];
         bool over = false;
+        uint64_t z2[NB][2];  // (row 2t, row 2t + 1) of keys g and g + 8
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            z2[nb][e] = fmul2(f2_pack(sc[nb][2 * e], sc[nb][2 * e + 1]),
+                              f2_pack(rowf[2 * nb] * ks[e], rowf[2 * nb + 1] * ks[e]));
+        if constexpr (CAP) {
+          // the polynomial within its range: the exponential form's error is
+          // 6e-8 of the cap even where the scores are small
+          float ax = 0.f;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float a, b;
+              f2_unpack(z2[nb][e], a, b);
+              ax = fmax3(ax, fabsf(a), fabsf(b));
+            }
+          const uint64_t cl2 = f2_pack(p.cap_log2, p.cap_log2);
+          if (__all_sync(0xffffffffu, ax <= kTanhRange)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) z2[nb][e] = fmul2(tanh2_poly(z2[nb][e]), cl2);
+          } else {
+            const uint64_t xe2 = f2_pack(kTwoLog2e, kTwoLog2e), cm2 = f2_pack(-2.f * p.cap_log2, -2.f * p.cap_log2);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) z2[nb][e] = tanh2_any(fmul2(z2[nb][e], xe2), cl2, cm2);
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          f2_unpack(z2[nb][0], sc[nb][0], sc[nb][1]);
+          f2_unpack(z2[nb][1], sc[nb][2], sc[nb][3]);
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int x = 2 * nb + (c & 1), key = k0 + g + 8 * (c >> 1);
-            float z = sc[nb][c] * (rowf[x] * ks[c >> 1]);
-            if (CAP) z = p.cap_log2 * tanh_any(z * kTwoLog2e);
+            float z = sc[nb][c];
             if (BIAS) z = fmaf(-slope[x], fabsf(static_cast<float>(pos[x] - key)), z);
             float zo = z + ev[c >> 1];
             if (!all_see) {

@@ -75,7 +75,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float tanh_any(float x2) { return fmaf(-2.f, rcp_approx(1.f + ex2(x2)), 1.f); }
 // base + mul / (1 + 2^x2) of a packed pair: with (1, -2) the tanh
 __device__ __forceinline__ uint64_t tanh2_any(uint64_t x2, uint64_t base, uint64_t mul) {
   float a, b;
