@@ -53,6 +53,8 @@ EXPORTS = {
     "fa_mod_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
     "fa_mod_bwd_workspace_size": (_S, [_I, _I, _I, _I, _I]),
     "fa_mod_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _F, _F, _P]),
+    "fa_mod_bwd_deterministic": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _F, _F,
+                                 _P]),
     "fa_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "fa_cache_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "fa_cache_decode_workspace_size": (_S, [_I, _I, _I, _I, _I, _I]),

@@ -18,6 +18,7 @@
 #include "fa_fwd.cuh"
 #include "fa_fwd_fp8.cuh"
 #include "fa_mod_bwd.cuh"
+#include "fa_mod_bwd_dq.cuh"
 #include "fa_mod_fwd.cuh"
 #include "fa_plan.cuh"
 
@@ -578,38 +579,115 @@ fa_status dispatch_mod_fwd(int dev, bool cap, bool bias, const CUtensorMap& q, c
   return bias ? launch_mod_fwd<D, false, true>(dev, q, k, v, p, s) : launch_mod_fwd<D, false, false>(dev, q, k, v, p, s);
 }
 
-template <int D, bool CAP, bool BIAS>
+// DET: dK and dV from the main kernel without its dQ product, dQ from its own pass
+// in a fixed order; else dQ through the fp32 accumulator and its conversion.
+template <int D, bool CAP, bool BIAS, bool DET>
 fa_status launch_mod_bwd(int dev, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                         const CUtensorMap& mdo, const fa::ModBwdParams& p, const fa::BwdParams& conv, cudaStream_t s) {
-  static bool done[kMaxDevices] = {};
-  auto kern = fa::fa_mod_bwd_kernel<D, CAP, BIAS>;
-  constexpr int smem = fa::ModBwdCfg<D>::SMEM_BYTES;
+                         const CUtensorMap& mdo, fa::ModBwdParams p, cudaStream_t s) {
+  static bool done[kMaxDevices] = {}, done_dq[kMaxDevices] = {};
+  auto kern = fa::fa_mod_bwd_kernel<D, CAP, BIAS, !DET>;
+  constexpr int smem = fa::ModBwdCfg<D>::SMEM_BYTES, smem_dq = fa::DqCfg<D>::SMEM_BYTES;
   fa_status st = ensure_smem(kern, dev, smem, done, fa::BwdCfg<D>::LAUNCH_REGS);
   if (st != FA_OK) return st;
+  if constexpr (DET) {
+    if ((st = ensure_smem(fa::fa_mod_bwd_dq_kernel<D, CAP, BIAS>, dev, smem_dq, done_dq)) != FA_OK) return st;
+    p.dq_acc = nullptr;
+  }
   const int64_t grid = static_cast<int64_t>(p.T) * p.B * p.Hv;
+  const int64_t dq_grid = static_cast<int64_t>(p.T) * p.B * p.H;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.H * ((p.N + 31) / 32);
   const int64_t red = (static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4) + 255) / 256;
-  if (grid > 0x7fffffff || blocks > 0x7fffffff || red > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  if (dq_grid > 0x7fffffff || blocks > 0x7fffffff || red > 0x7fffffff) return FA_ERR_INVALID_ARG;
   mark_launch(s);
   fa::fa_mod_bwd_preprocess_kernel<D><<<preprocess_blocks(dev), 256, 0, s>>>(p);
   if ((st = launch_status(s)) != FA_OK) return st;
   kern<<<static_cast<unsigned>(grid), fa::BwdCfg<D>::THREADS, smem, s>>>(mq, mk, mv, mdo, p);
   if ((st = launch_status(s)) != FA_OK) return st;
-  fa::fa_bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(conv);
+  if constexpr (DET) {
+    fa::fa_mod_bwd_dq_kernel<D, CAP, BIAS>
+        <<<static_cast<unsigned>(dq_grid), fa::DqCfg<D>::THREADS, smem_dq, s>>>(mq, mk, mv, mdo, p);
+  } else {
+    fa::BwdParams conv = {};  // what the dQ conversion reads
+    conv.dq = p.dq;
+    conv.dq_acc = p.dq_acc;
+    conv.N = p.N;
+    conv.H = p.H;
+    conv.scale = p.scale;
+    fa::fa_bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(conv);
+  }
   if ((st = launch_status(s)) != FA_OK || !p.dk_part) return st;
   fa::fa_mod_bwd_reduce_kernel<<<dim3(static_cast<unsigned>(red), 2), 256, 0, s>>>(p, D);
   return launch_status(s);
 }
 
-template <int D>
+template <int D, bool DET>
 fa_status dispatch_mod_bwd(int dev, bool cap, bool bias, const CUtensorMap& q, const CUtensorMap& k,
-                           const CUtensorMap& v, const CUtensorMap& d_o, const fa::ModBwdParams& p,
-                           const fa::BwdParams& conv, cudaStream_t s) {
+                           const CUtensorMap& v, const CUtensorMap& d_o, const fa::ModBwdParams& p, cudaStream_t s) {
   if (cap)
-    return bias ? launch_mod_bwd<D, true, true>(dev, q, k, v, d_o, p, conv, s)
-                : launch_mod_bwd<D, true, false>(dev, q, k, v, d_o, p, conv, s);
-  return bias ? launch_mod_bwd<D, false, true>(dev, q, k, v, d_o, p, conv, s)
-              : launch_mod_bwd<D, false, false>(dev, q, k, v, d_o, p, conv, s);
+    return bias ? launch_mod_bwd<D, true, true, DET>(dev, q, k, v, d_o, p, s)
+                : launch_mod_bwd<D, true, false, DET>(dev, q, k, v, d_o, p, s);
+  return bias ? launch_mod_bwd<D, false, true, DET>(dev, q, k, v, d_o, p, s)
+              : launch_mod_bwd<D, false, false, DET>(dev, q, k, v, d_o, p, s);
+}
+
+fa_status mod_bwd_common(const void* q, const void* k, const void* v, const void* o, const void* o_low, const float* lse,
+                         const void* dO, void* dq, void* dk, void* dv, const void* plan, const float* slopes,
+                         void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
+                         void* stream, bool det) {
+  const void* ptrs[] = {q, k, v, o, lse, dO, dq, dk, dv, workspace};
+  for (const void* ptr : ptrs)
+    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(o_low) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_INVALID_ARG;
+  int dev;
+  fa_status st = mod_check(B, N, H, Hkv, d, scale, softcap, plan, slopes);
+  if (st != FA_OK) return st;
+  const ModBwdWs wl = mod_bwd_ws(B, N, H, Hkv, d);
+  if (ws_bytes < wl.total) return FA_ERR_WORKSPACE;
+  if ((st = current_device(&dev)) != FA_OK) return st;
+  CUtensorMap mq, mk, mv, mdo;
+  if ((st = make_map_bf16(&mq, q, d, H, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mk, k, d, Hkv, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mv, v, d, Hkv, N, B, 128)) != FA_OK) return st;
+  if ((st = make_map_bf16(&mdo, dO, d, H, N, B, 128)) != FA_OK) return st;
+  fa::ModBwdParams p;
+  p.o = o;
+  p.o_low = o_low;
+  p.dout = dO;
+  p.lse = lse;
+  p.slopes = slopes;
+  p.dk = dk;
+  p.dv = dv;
+  char* ws = static_cast<char*>(workspace);
+  p.dq_acc = reinterpret_cast<float*>(ws);
+  p.dvec = reinterpret_cast<float*>(ws + wl.dvec);
+  const int parts = mod_bwd_parts(B, N, H, Hkv);
+  p.dk_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.dk_part) : nullptr;
+  p.dv_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.dv_part) : nullptr;
+  p.Hv = Hkv * parts;
+  p.hs = H / p.Hv;
+  p.plan = plan_view(plan, B, N);
+  p.B = B;
+  p.N = N;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = H / Hkv;
+  p.T = (N + 127) / 128;
+  const int64_t pairs = static_cast<int64_t>(B) * p.Hv;
+  if (pairs > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  p.group = static_cast<int>(pairs);
+  if (pairs * p.T > 4096) p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.hs, pairs);  // Q, dO, dQ acc
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
+  p.cap_log2 = softcap * kLog2e;
+  p.dq = dq;
+  const bool cap = softcap > 0.f, bias = slopes != nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (det)
+    return d == 64 ? dispatch_mod_bwd<64, true>(dev, cap, bias, mq, mk, mv, mdo, p, s)
+                   : dispatch_mod_bwd<128, true>(dev, cap, bias, mq, mk, mv, mdo, p, s);
+  return d == 64 ? dispatch_mod_bwd<64, false>(dev, cap, bias, mq, mk, mv, mdo, p, s)
+                 : dispatch_mod_bwd<128, false>(dev, cap, bias, mq, mk, mv, mdo, p, s);
 }
 
 // ------------------------------------------------------------- 8-bit cache
@@ -931,61 +1009,17 @@ fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o,
                      void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
                      void* stream) {
   LaunchEventsScope hook_scope;
-  const void* ptrs[] = {q, k, v, o, lse, dO, dq, dk, dv, workspace};
-  for (const void* ptr : ptrs)
-    if (!ptr || !aligned16(ptr)) return FA_ERR_INVALID_ARG;
-  if (!aligned16(o_low) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_INVALID_ARG;
-  int dev;
-  fa_status st = mod_check(B, N, H, Hkv, d, scale, softcap, plan, slopes);
-  if (st != FA_OK) return st;
-  const ModBwdWs wl = mod_bwd_ws(B, N, H, Hkv, d);
-  if (ws_bytes < wl.total) return FA_ERR_WORKSPACE;
-  if ((st = current_device(&dev)) != FA_OK) return st;
-  CUtensorMap mq, mk, mv, mdo;
-  if ((st = make_map_bf16(&mq, q, d, H, N, B, 128)) != FA_OK) return st;
-  if ((st = make_map_bf16(&mk, k, d, Hkv, N, B, 128)) != FA_OK) return st;
-  if ((st = make_map_bf16(&mv, v, d, Hkv, N, B, 128)) != FA_OK) return st;
-  if ((st = make_map_bf16(&mdo, dO, d, H, N, B, 128)) != FA_OK) return st;
-  fa::ModBwdParams p;
-  p.o = o;
-  p.o_low = o_low;
-  p.dout = dO;
-  p.lse = lse;
-  p.slopes = slopes;
-  p.dk = dk;
-  p.dv = dv;
-  char* ws = static_cast<char*>(workspace);
-  p.dq_acc = reinterpret_cast<float*>(ws);
-  p.dvec = reinterpret_cast<float*>(ws + wl.dvec);
-  const int parts = mod_bwd_parts(B, N, H, Hkv);
-  p.dk_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.dk_part) : nullptr;
-  p.dv_part = parts > 1 ? reinterpret_cast<float*>(ws + wl.dv_part) : nullptr;
-  p.Hv = Hkv * parts;
-  p.hs = H / p.Hv;
-  p.plan = plan_view(plan, B, N);
-  p.B = B;
-  p.N = N;
-  p.H = H;
-  p.Hkv = Hkv;
-  p.G = H / Hkv;
-  p.T = (N + 127) / 128;
-  const int64_t pairs = static_cast<int64_t>(B) * p.Hv;
-  if (pairs > 0x7fffffff) return FA_ERR_INVALID_ARG;
-  p.group = static_cast<int>(pairs);
-  if (pairs * p.T > 4096) p.group = head_group(static_cast<int64_t>(N) * d * (2 + 2 + 4) * p.hs, pairs);  // Q, dO, dQ acc
-  p.scale = scale;
-  p.scale_log2 = scale * kLog2e;
-  p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
-  p.cap_log2 = softcap * kLog2e;
-  fa::BwdParams conv = {};  // what the dQ conversion reads
-  conv.dq = dq;
-  conv.dq_acc = p.dq_acc;
-  conv.N = N;
-  conv.H = H;
-  conv.scale = scale;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d == 64 ? dispatch_mod_bwd<64>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, mdo, p, conv, s)
-                 : dispatch_mod_bwd<128>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, mdo, p, conv, s);
+  return mod_bwd_common(q, k, v, o, o_low, lse, dO, dq, dk, dv, plan, slopes, workspace, ws_bytes, B, N, H, Hkv, d,
+                        scale, softcap, stream, false);
+}
+
+fa_status fa_mod_bwd_deterministic(const void* q, const void* k, const void* v, const void* o, const void* o_low,
+                                   const float* lse, const void* dO, void* dq, void* dk, void* dv, const void* plan,
+                                   const float* slopes, void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv,
+                                   int d, float scale, float softcap, void* stream) {
+  LaunchEventsScope hook_scope;
+  return mod_bwd_common(q, k, v, o, o_low, lse, dO, dq, dk, dv, plan, slopes, workspace, ws_bytes, B, N, H, Hkv, d,
+                        scale, softcap, stream, true);
 }
 
 fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scale, void* v_scale,

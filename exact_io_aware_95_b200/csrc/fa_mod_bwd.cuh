@@ -66,7 +66,8 @@ struct ModBwdParams {
   void* dv;
   float* dk_part;       // fp32 [B, N, Hv, d] partial dK (unscaled) and dV when a
   float* dv_part;       // group's heads are split, else nullptr
-  float* dq_acc;        // layout: dq_acc_index4()
+  float* dq_acc;        // layout: dq_acc_index4(); nullptr: dQ has a pass of its own
+  void* dq;             // written by that pass
   float* dvec;          // fp32 D [B, H, N]
   PlanView plan;
   int B, N, H, Hkv, G;
@@ -75,6 +76,33 @@ struct ModBwdParams {
   int group;            // (entry, heads) pairs per scheduling group
   float scale, scale_log2, x_mul, cap_log2;
 };
+
+// 32 scores of a thread (raw products) become tanh(x / cap); the whole warp calls
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[32], float x_mul) {
+  float ax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) ax = fmax3(ax, fabsf(__uint_as_float(s[e])), fabsf(__uint_as_float(s[e + 1])));
+  if (__all_sync(0xffffffffu, ax * fabsf(x_mul) <= kTanhRange)) {
+    const uint64_t xm2 = f2_pack(x_mul, x_mul);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float a, b;
+      f2_unpack(tanh2_poly(fmul2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), xm2)), a, b);
+      s[e] = __float_as_uint(a);
+      s[e + 1] = __float_as_uint(b);
+    }
+  } else {
+    const uint64_t xe2 = f2_pack(x_mul * kTwoLog2e, x_mul * kTwoLog2e);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float a, b;
+      f2_unpack(tanh2_any(fmul2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), xe2), f2_pack(1.f, 1.f),
+                          f2_pack(-2.f, -2.f)), a, b);
+      s[e] = __float_as_uint(a);
+      s[e + 1] = __float_as_uint(b);
+    }
+  }
+}
 
 // D = rowsum(dO (O + O_low)) and the zeroed dQ accumulator; the shape of
 // fa_bwd_preprocess_kernel.
@@ -87,7 +115,8 @@ __global__ void __launch_bounds__(256) fa_mod_bwd_preprocess_kernel(const ModBwd
   const int64_t nrows = static_cast<int64_t>(p.B) * p.N * p.H;
   const int64_t nacc4 = nrows * (D / 4);
   float4* acc = reinterpret_cast<float4*>(p.dq_acc);
-  for (int64_t i = gtid; i < nacc4; i += nthreads) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (acc)
+    for (int64_t i = gtid; i < nacc4; i += nthreads) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, part = lane % LPR;
   const int64_t nwarps = nthreads >> 5;
@@ -170,7 +199,10 @@ __device__ __forceinline__ void mod_bwd_item(const ModBwdParams& p, int c, ModBw
   it.niter = it.ni * p.hs;
 }
 
-template <int D, bool CAP, bool BIAS>
+// DQ: also form dQ_i = dS K_j per tile and add it into the fp32 accumulator
+// (atomic, order varies); without it the kernel computes dK and dV only and
+// fa_mod_bwd_dq.cuh sums dQ in a fixed order.
+template <int D, bool CAP, bool BIAS, bool DQ>
 __global__ void __launch_bounds__(512, 1)
     fa_mod_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -359,7 +391,7 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_after();
         issue_s(gt0);
         // at d = 128 the first dP^T reuses the columns of the previous item's last dQ
-        if (C::DQ_ALIASES_DP && gt0 > 0) {
+        if (DQ && C::DQ_ALIASES_DP && gt0 > 0) {
           if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), (gt0 - 1) & 1, abort_flag))) break;
           tc_fence_after();
         }
@@ -395,21 +427,23 @@ __global__ void __launch_bounds__(512, 1)
           for (int kk = 0; kk < 8; ++kk)
             umma_ss(tmem + C::TM_DK, sdesc_adv(dS_k, (kk >> 2) * 16384 + (kk & 3) * 32), sdesc_adv(q_mn, kk * 2048),
                     kIdDV, (it > 0 || kk > 0));
-          if (!C::DQ_ALIASES_DP && gt > 0) {
-            if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), par ^ 1u, abort_flag))) break;
-            tc_fence_after();
-          }
+          if constexpr (DQ) {
+            if (!C::DQ_ALIASES_DP && gt > 0) {
+              if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), par ^ 1u, abort_flag))) break;
+              tc_fence_after();
+            }
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ss(tmem + C::TM_DQ, sdesc_adv(dS_mn, kk * 2048), sdesc_adv(dK_mn, kk * 2048), kIdDQ, kk > 0);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ss(tmem + C::TM_DQ, sdesc_adv(dS_mn, kk * 2048), sdesc_adv(dK_mn, kk * 2048), kIdDQ, kk > 0);
+          }
           umma_commit(bar(C::BAR_QDO_EMPTY + st));
           umma_commit(bar(C::BAR_DS_EMPTY));
-          umma_commit(bar(C::BAR_DQ_FULL));
+          if (DQ) umma_commit(bar(C::BAR_DQ_FULL));
           // dP^T of the next query tile: the P/dS warps finished reading dP^T(i)
           // before they signalled dS^T(i); at d = 128 its columns also hold dQ(i),
           // so wait until the drain has loaded it (completion i of DQ_EMPTY)
           if (it + 1 < niter) {
-            if (C::DQ_ALIASES_DP) {
+            if (DQ && C::DQ_ALIASES_DP) {
               if (!(ok = mbar_wait(bar(C::BAR_DQ_EMPTY), par, abort_flag))) break;
               tc_fence_after();
             }
@@ -525,33 +559,7 @@ __global__ void __launch_bounds__(512, 1)
           uint32_t s[32];
           tmem_ld32(lane_base + C::TM_S + 32 * cc, s);
           tmem_wait_ld(s);
-          if constexpr (CAP) {  // s becomes t = tanh(x / cap)
-            float ax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              ax = fmax3(ax, fabsf(__uint_as_float(s[e])), fabsf(__uint_as_float(s[e + 1])));
-            if (__all_sync(0xffffffffu, ax * fabsf(p.x_mul) <= kTanhRange)) {
-              const uint64_t xm2 = f2_pack(p.x_mul, p.x_mul);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float a, b;
-                f2_unpack(tanh2_poly(fmul2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), xm2)), a, b);
-                s[e] = __float_as_uint(a);
-                s[e + 1] = __float_as_uint(b);
-              }
-            } else {
-              const float xe = p.x_mul * kTwoLog2e;
-              const uint64_t xe2 = f2_pack(xe, xe);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float a, b;
-                f2_unpack(tanh2_any(fmul2(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), xe2),
-                                    f2_pack(1.f, 1.f), f2_pack(-2.f, -2.f)), a, b);
-                s[e] = __float_as_uint(a);
-                s[e + 1] = __float_as_uint(b);
-              }
-            }
-          }
+          if constexpr (CAP) cap_scores(s, p.x_mul);  // s becomes t = tanh(x / cap)
           // Everything that depends on the tile is decided outside the column
           // loop (a branch in it, even one rarely taken, keeps the columns from
           // being scheduled together: 1477 us against 1172 at 2 x 16 x 8192 x 64).
@@ -716,7 +724,7 @@ __global__ void __launch_bounds__(512, 1)
       if (!__all_sync(0xffffffffu, ok) || item < 0) break;
       ModBwdItem I;
       mod_bwd_item(p, item, I);
-      {
+      if constexpr (DQ) {
         int h = I.hv * p.hs, i = 0;
         for (int it = 0; it < I.niter; ++it) {
           const uint32_t par = (gt0 + it) & 1;

@@ -134,9 +134,11 @@ def mod_bwd_workspace_size(B: int, N: int, H: int, Hkv: int, d: int) -> int:
 
 def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
             scale: Optional[float] = None, o_low: Optional[torch.Tensor] = None,
-            workspace: Optional[torch.Tensor] = None, dq=None, dk=None, dv=None):
+            workspace: Optional[torch.Tensor] = None, dq=None, dk=None, dv=None, deterministic: bool = False):
     """dQ [B, N, H, d], dK and dV [B, N, Hkv, d] (summed over each group of heads);
-    o, lse (and o_low) from mod_fwd with the same plan, softcap, slopes and scale."""
+    o, lse (and o_low) from mod_fwd with the same plan, softcap, slopes and scale.
+
+    deterministic=True: dQ too is bitwise reproducible (dK and dV always are)."""
     B, N, H, Hkv, d = _sizes(q, k, v, plan)
     softcap = _softcap(softcap)
     _slopes(slopes, H)
@@ -161,21 +163,21 @@ def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: O
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(k) if dv is None else dv
     with _on(q):
-        st = L.fa_mod_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                          None if o_low is None else o_low.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
-                          dk.data_ptr(), dv.data_ptr(), plan.data.data_ptr(),
-                          None if slopes is None else slopes.data_ptr(), ws.data_ptr(), ws.nbytes, B, N, H, Hkv, d,
-                          _scale(scale, d), softcap, _stream_ptr(q))
-    _check(st, "fa_mod_bwd")
+        fn = L.fa_mod_bwd_deterministic if deterministic else L.fa_mod_bwd
+        st = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), None if o_low is None else o_low.data_ptr(),
+                lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), plan.data.data_ptr(),
+                None if slopes is None else slopes.data_ptr(), ws.data_ptr(), ws.nbytes, B, N, H, Hkv, d,
+                _scale(scale, d), softcap, _stream_ptr(q))
+    _check(st, "fa_mod_bwd_deterministic" if deterministic else "fa_mod_bwd")
     return dq, dk, dv
 
 
 class _ModAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, plan, softcap, slopes, scale):
+    def forward(ctx, q, k, v, plan, softcap, slopes, scale, deterministic):
         o, lse, o_low = mod_fwd(q, k, v, plan, softcap=softcap, slopes=slopes, scale=scale, low=True)
         ctx.save_for_backward(q, k, v, o, lse, o_low, plan.data, *(() if slopes is None else (slopes,)))
-        ctx.sizes, ctx.softcap, ctx.scale = (plan.B, plan.N), softcap, scale
+        ctx.sizes, ctx.softcap, ctx.scale, ctx.deterministic = (plan.B, plan.N), softcap, scale, deterministic
         return o
 
     @staticmethod
@@ -183,16 +185,19 @@ class _ModAttention(torch.autograd.Function):
     def backward(ctx, do):
         q, k, v, o, lse, o_low, data, *slopes = ctx.saved_tensors
         g = mod_bwd(q, k, v, o, lse, do.contiguous(), MaskPlan(data, *ctx.sizes), softcap=ctx.softcap,
-                    slopes=slopes[0] if slopes else None, scale=ctx.scale, o_low=o_low)
-        return (*g, None, None, None, None)
+                    slopes=slopes[0] if slopes else None, scale=ctx.scale, o_low=o_low,
+                    deterministic=ctx.deterministic)
+        return (*g, None, None, None, None, None)
 
 
 def mod_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskPlan, softcap: float = 0.0,
-                  slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None) -> torch.Tensor:
+                  slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  deterministic: bool = False) -> torch.Tensor:
     """Attention with modified scores over bf16 [B, N, H, d] queries and
-    [B, N, Hkv, d] keys and values; differentiable in q, k, v."""
+    [B, N, Hkv, d] keys and values; differentiable in q, k, v.
+    deterministic=True makes the gradients bitwise reproducible."""
     if isinstance(q, torch.Tensor) and q.dim() == 4:
         _slopes(slopes, q.shape[2])  # inside a Function no tensor asks for a gradient
     if not (torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (q, k, v))):
         return mod_fwd(q, k, v, plan, softcap=softcap, slopes=slopes, scale=scale)[0]
-    return _ModAttention.apply(q, k, v, plan, softcap, slopes, scale)
+    return _ModAttention.apply(q, k, v, plan, softcap, slopes, scale, bool(deterministic))

@@ -219,13 +219,22 @@ fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void*
  * same plan, slopes, scale and softcap.  dq: bf16 [B, N, H, d]; dk, dv: bf16
  * [B, N, Hkv, d], summed over the heads of the group.  workspace: ws_bytes >=
  * fa_mod_bwd_workspace_size(B, N, H, Hkv, d), 256-byte aligned.  dK and dV are
- * bitwise reproducible; dQ is accumulated with fp32 atomics as in fa_bwd.
+ * bitwise reproducible; dQ is accumulated with fp32 atomics as in fa_bwd
+ * (fa_mod_bwd_deterministic: in a fixed order).
  * The slopes are constants: they get no gradient. */
 size_t fa_mod_bwd_workspace_size(int B, int N, int H, int Hkv, int d);
 fa_status fa_mod_bwd(const void* q, const void* k, const void* v, const void* o, const void* o_low, const float* lse,
                      const void* dO, void* dq, void* dk, void* dv, const void* plan, const float* slopes,
                      void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv, int d, float scale, float softcap,
                      void* stream);
+
+/* Deterministic backward: arguments, workspace and errors of fa_mod_bwd; dQ is
+ * summed in a fixed order by a pass of its own, without atomics, so all three
+ * gradients are bitwise reproducible. */
+fa_status fa_mod_bwd_deterministic(const void* q, const void* k, const void* v, const void* o, const void* o_low,
+                                   const float* lse, const void* dO, void* dq, void* dk, void* dv, const void* plan,
+                                   const float* slopes, void* workspace, size_t ws_bytes, int B, int N, int H, int Hkv,
+                                   int d, float scale, float softcap, void* stream);
 
 /* ---- 8-bit key/value cache ----------------------------------------------------
  * A cache is e4m3 codes [B, Nk, Hkv, d] and one exponent byte per row,

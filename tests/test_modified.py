@@ -132,8 +132,17 @@ def check(x, mask, softcap=0.0, slopes=None, low=True):
     grads = [torch.full_like(g[n], float("nan")) for n in ("q", "k", "v")]
     fa.mod_bwd(g["q"], g["k"], g["v"], outs[0], lse, g["do"], plan, o_low=outs[1] if low else None, dq=grads[0],
                dk=grads[1], dv=grads[2], **how)
+    det = [torch.full_like(g[n], float("nan")) for n in ("q", "k", "v")]
+    fa.mod_bwd(g["q"], g["k"], g["v"], outs[0], lse, g["do"], plan, o_low=outs[1] if low else None, dq=det[0],
+               dk=det[1], dv=det[2], deterministic=True, **how)
     fa.check_device_error()
     assert len(r) == (3 if low else 2)
+    # the fixed-order pass: the same dK and dV, and dQ from the same terms
+    assert torch.equal(det[1], grads[1]) and torch.equal(det[2], grads[2])
+    if low:
+        assert not torch.isnan(det[0]).any()
+        again = fa.mod_bwd(g["q"], g["k"], g["v"], outs[0], lse, g["do"], plan, o_low=outs[1], deterministic=True, **how)
+        assert all(torch.equal(a, b) for a, b in zip(again, det))
     got = dict(zip(("o", "dq", "dk", "dv"), (f64(t) for t in (outs[0], *grads))))
     a = [f64(x[n]) for n in ("q", "k", "v")]
     want = {}
@@ -144,6 +153,8 @@ def check(x, mask, softcap=0.0, slopes=None, low=True):
     assert np.array_equal(np.isneginf(l64), np.isneginf(L))
     fin = np.isfinite(L)
     assert np.all(np.abs(l64[fin] - L[fin]) <= tol["lse"][fin])
+    if low:
+        assert (np.abs(f64(det[0]) - want["dq"]) - tol["dq"]).max() <= 0
     for n in want:
         if low or n in ("o", "dv"):
             over = np.abs(got[n] - want[n]) - tol[n]
@@ -282,6 +293,7 @@ def test_library_refuses_bad_arguments():
     assert L.fa_mod_bwd(*at(b, 12, P + 16), ws, 1, 8, 2, 1, 64, 1.0, 0.0, None) == inv
     for i in (0, 1, 2, 3, 5, 6, 7, 8, 9, 10, 12):
         assert L.fa_mod_bwd(*at(b, i, None), ws, 1, 8, 2, 1, 64, 1.0, 0.0, None) == inv
+        assert L.fa_mod_bwd_deterministic(*at(b, i, None), ws, 1, 8, 2, 1, 64, 1.0, 0.0, None) == inv
 
 
 # --------------------------------------------------------------- GPU: parity
@@ -490,6 +502,40 @@ def test_autograd():
         assert torch.equal(fa.mod_attention(q, k, v, plan, softcap=30.0, slopes=sl), o)
     assert torch.equal(o, o1)
     assert torch.equal(k.grad, g[1]) and torch.equal(v.grad, g[2]) and rel_fro(f64(q.grad), f64(g[0])) <= U
+
+
+@pytest.mark.gpu
+def test_deterministic_gradients():
+    # many key tiles add into each dQ row, so an order that varied would show
+    x = make(2, 1500, 8, 2, 64, 31)
+    q, k, v = (x[n].cuda().requires_grad_(True) for n in ("q", "k", "v"))
+    do, sl = x["do"].cuda(), slopes_of(8).cuda()
+    ids = docs_of(2, 1500, 9, 900).cuda()
+
+    def step():
+        plan = fa.mask_plan(2, 1500, doc_ids=ids)
+        o = fa.mod_attention(q, k, v, plan, softcap=20.0, slopes=sl, deterministic=True)
+        return torch.autograd.grad(o, (q, k, v), do)
+
+    want = step()
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(step(), want))
+    with torch.no_grad():
+        plan = fa.mask_plan(2, 1500, doc_ids=ids)
+        o, lse, low = fa.mod_fwd(q, k, v, plan, softcap=20.0, slopes=sl, low=True)
+
+        def back():
+            return fa.mod_bwd(q, k, v, o, lse, do, plan, softcap=20.0, slopes=sl, o_low=low, deterministic=True)
+
+        assert all(torch.equal(a, b) for a, b in zip(back(), want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = back()
+        for t in held:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
 
 
 @pytest.mark.gpu
