@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -200,13 +201,14 @@ fa_status launch_status(cudaStream_t s) {
 // placed while the kernel before it on the stream ends, and wait for its end
 // (griddepcontrol.wait) before they read.
 template <typename... P, typename... A>
-fa_status launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t s, A... args) {
+fa_status launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -596,28 +598,35 @@ fa_status launch_mod_bwd(int dev, const CUtensorMap& mq, const CUtensorMap& mk, 
   const int64_t grid = static_cast<int64_t>(p.T) * p.B * p.Hv;
   const int64_t dq_grid = static_cast<int64_t>(p.T) * p.B * p.H;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.H * ((p.N + 31) / 32);
-  const int64_t red = (static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4) + 255) / 256;
-  if (dq_grid > 0x7fffffff || blocks > 0x7fffffff || red > 0x7fffffff) return FA_ERR_INVALID_ARG;
+  const int64_t red = p.dk_part ? (static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4) + 255) / 256 : 0;
+  const int64_t finish = (DET ? 0 : blocks) + 2 * red;
+  if (dq_grid > 0x7fffffff || finish > 0x7fffffff) return FA_ERR_INVALID_ARG;
   mark_launch(s);
-  fa::fa_mod_bwd_preprocess_kernel<D><<<preprocess_blocks(dev), 256, 0, s>>>(p);
+  // no more blocks than there are 16-byte pieces of dQ: short calls start fewer
+  const int64_t pieces = (static_cast<int64_t>(p.B) * p.N * p.H * (D / 4) + 255) / 256;
+  const unsigned pre = static_cast<unsigned>(std::min<int64_t>(preprocess_blocks(dev), pieces));
+  fa::fa_mod_bwd_preprocess_kernel<D><<<pre, 256, 0, s>>>(p);
   if ((st = launch_status(s)) != FA_OK) return st;
-  kern<<<static_cast<unsigned>(grid), fa::BwdCfg<D>::THREADS, smem, s>>>(mq, mk, mv, mdo, p);
-  if ((st = launch_status(s)) != FA_OK) return st;
+  if ((st = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), fa::BwdCfg<D>::THREADS, smem, s, mq, mk, mv, mdo,
+                             p)) != FA_OK)
+    return st;
+  mark_launch(s);
   if constexpr (DET) {
     fa::fa_mod_bwd_dq_kernel<D, CAP, BIAS>
         <<<static_cast<unsigned>(dq_grid), fa::DqCfg<D>::THREADS, smem_dq, s>>>(mq, mk, mv, mdo, p);
-  } else {
-    fa::BwdParams conv = {};  // what the dQ conversion reads
-    conv.dq = p.dq;
-    conv.dq_acc = p.dq_acc;
-    conv.N = p.N;
-    conv.H = p.H;
-    conv.scale = p.scale;
-    fa::fa_bwd_dq_convert_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, s>>>(conv);
+    if ((st = launch_status(s)) != FA_OK) return st;
   }
-  if ((st = launch_status(s)) != FA_OK || !p.dk_part) return st;
-  fa::fa_mod_bwd_reduce_kernel<<<dim3(static_cast<unsigned>(red), 2), 256, 0, s>>>(p, D);
-  return launch_status(s);
+  if (finish == 0) return FA_OK;
+  fa::BwdParams conv = {};  // what the dQ conversion reads
+  conv.dq = p.dq;
+  conv.dq_acc = p.dq_acc;
+  conv.N = p.N;
+  conv.H = p.H;
+  conv.scale = p.scale;
+  st = launch_dependent(fa::fa_mod_bwd_finish_kernel<D>, dim3(static_cast<unsigned>(finish)), 256, 0, s, p, conv,
+                        static_cast<unsigned>(DET ? 0 : blocks), static_cast<unsigned>(red));
+  if (st == FA_OK) mark_launch(s);
+  return st;
 }
 
 template <int D, bool DET>
@@ -747,7 +756,7 @@ fa_status launch_cache_decode(int dev, const CUtensorMap& mk, const CUtensorMap&
   if ((st = launch_status(s)) != FA_OK) return st;
   const dim3 merge(static_cast<unsigned>(p.by_segment ? segments : p.groups) * p.Hkv, p.rows < p.rpb ? p.rows : p.rpb);
   // records of a segment: about groups / segments.  Few: small blocks, all of them resident at once
-  st = launch_dependent(fa::fa_cache_decode_merge_kernel<D>, merge, segments * 8 < p.groups ? 512 : 128, s, p);
+  st = launch_dependent(fa::fa_cache_decode_merge_kernel<D>, merge, segments * 8 < p.groups ? 512 : 128, 0, s, p);
   return st != FA_OK ? st : launch_status(s);
 }
 
@@ -960,7 +969,7 @@ fa_status fa_mask_plan(void* plan, size_t plan_bytes, const int* doc_ids, const 
   const dim3 grid((N + fa::kPlanThreads - 1) / fa::kPlanThreads, B);
   fa::fa_mask_plan_kernel<<<grid, fa::kPlanThreads, 0, s>>>(pv, doc_ids, prefix_len, N, window, causal);
   if ((st = launch_status(s)) != FA_OK || grid.x == 1) return st;
-  st = launch_dependent(fa::fa_mask_plan_tiles_kernel, dim3((T + 3) / 4, B), 128, s, pv, T);
+  st = launch_dependent(fa::fa_mask_plan_tiles_kernel, dim3((T + 3) / 4, B), 128, 0, s, pv, T);
   return st != FA_OK ? st : launch_status(s);
 }
 

@@ -10,7 +10,9 @@
 //     dQ_i  = scale sum dS_ij k_j
 //
 // Three launches, as in the plain backward (fa_bwd.cuh): D and the zeroed fp32
-// dQ accumulator; the fused main kernel; dQ to bf16.  The main kernel is the
+// dQ accumulator; the fused main kernel; dQ to bf16.  The second and third are
+// launched as dependents of the one before (2 x 8(1) x 2047 x 64, window: 66 us
+// with four plain launches, 63 so; 1 x 2(1) x 130 x 64: 25 and 22).  The main kernel is the
 // plain one's pipeline (same warps, barriers, tensor-memory columns and
 // products, S^T form with one key per lane) with these differences:
 //   - a work item is (128-key tile, batch entry, key head); the CTA walks the
@@ -20,7 +22,7 @@
 //     fixed order.  A key tile no query sees is stored as zero.  Where that
 //     makes too few items for the SMs (few key heads, short sequences) the host
 //     splits each group's heads over several items; those store fp32 partial
-//     sums, and a last kernel adds them in a fixed order: 2 x 8 heads on one key
+//     sums, and the last kernel adds them in a fixed order: 2 x 8 heads on one key
 //     head x 2047 tokens, window 512, takes 32 items whole (181 us) and 256
 //     split;
 //   - D takes O with its rounding residual when the caller has it: with O in
@@ -249,6 +251,12 @@ __global__ void __launch_bounds__(512, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
+  // D and the zeroed accumulator are there.  No memory clobber: the barrier below
+  // keeps every access after this, and with one the bias variants spill 40 bytes
+  // instead of 16.  The kernel before this one does not call for its dependents
+  // early: CTAs placed while it still runs took the long first items unevenly
+  // (2 x 16 x 8192 x 64 with documents: 281 us against 273).
+  asm volatile("griddepcontrol.wait;" ::);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -783,15 +791,27 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-// dK = scale * sum, dV = sum of the group's partial sums, in the order of the
-// heads.  One thread per four columns; blockIdx.y: keys or values.
-__global__ void __launch_bounds__(256) fa_mod_bwd_reduce_kernel(const ModBwdParams p, int D) {
+// What is left after the main kernel, in one launch.  Blocks below nconv: dQ to
+// bf16.  The others, where a group's heads were split: dK = scale * sum, dV = sum
+// of the group's partial sums, in the order of the heads; one thread per four
+// columns, first the keys, then the values.
+template <int D>
+__global__ void __launch_bounds__(256) fa_mod_bwd_finish_kernel(const ModBwdParams p, const BwdParams conv,
+                                                               unsigned nconv, unsigned nred) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel has ended and its sums are visible
+  if (blockIdx.x < nconv) {
+    dq_convert_block<D>(conv, blockIdx.x);
+    return;
+  }
   const int64_t n4 = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  unsigned blk = blockIdx.x - nconv;
+  const bool values = blk >= nred;
+  if (values) blk -= nred;
+  const int64_t i = static_cast<int64_t>(blk) * 256 + threadIdx.x;
   if (i >= n4) return;
   const int parts = p.Hv / p.Hkv, q = D / 4;
   const int64_t row = i / q;  // (token, key head); its partials are rows row * parts ..
-  const float4* src = reinterpret_cast<const float4*>(blockIdx.y ? p.dv_part : p.dk_part) + row * parts * q + i % q;
+  const float4* src = reinterpret_cast<const float4*>(values ? p.dv_part : p.dk_part) + row * parts * q + i % q;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int k = 0; k < parts; ++k) {
@@ -801,8 +821,8 @@ __global__ void __launch_bounds__(256) fa_mod_bwd_reduce_kernel(const ModBwdPara
     a.z += v.z;
     a.w += v.w;
   }
-  const float mul = blockIdx.y ? 1.f : p.scale;
-  reinterpret_cast<uint2*>(blockIdx.y ? p.dv : p.dk)[i] =
+  const float mul = values ? 1.f : p.scale;
+  reinterpret_cast<uint2*>(values ? p.dv : p.dk)[i] =
       make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
 }
 
