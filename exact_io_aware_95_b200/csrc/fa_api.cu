@@ -617,13 +617,7 @@ fa_status launch_mod_bwd(int dev, const CUtensorMap& mq, const CUtensorMap& mk, 
     if ((st = launch_status(s)) != FA_OK) return st;
   }
   if (finish == 0) return FA_OK;
-  fa::BwdParams conv = {};  // what the dQ conversion reads
-  conv.dq = p.dq;
-  conv.dq_acc = p.dq_acc;
-  conv.N = p.N;
-  conv.H = p.H;
-  conv.scale = p.scale;
-  st = launch_dependent(fa::fa_mod_bwd_finish_kernel<D>, dim3(static_cast<unsigned>(finish)), 256, 0, s, p, conv,
+  st = launch_dependent(fa::fa_mod_bwd_finish_kernel<D>, dim3(static_cast<unsigned>(finish)), 256, 0, s, p,
                         static_cast<unsigned>(DET ? 0 : blocks), static_cast<unsigned>(red));
   if (st == FA_OK) mark_launch(s);
   return st;

@@ -148,13 +148,13 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess_kernel(const BwdParams 
 // as 512-byte runs (32 rows of one 4-column group per warp), transposed through
 // shared memory, and written as whole rows (D * 2 contiguous bytes per row).
 template <int D>
-__device__ __forceinline__ void dq_convert_block(const BwdParams& p, unsigned block) {
+__global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const BwdParams p) {
   constexpr int G = D / 4;  // float4 groups per row
   __shared__ float4 tile[32][G + 1];
   const int64_t R = p.cu_seqlens ? p.total : p.N;
   const int64_t nblk = (R + 31) / 32;
-  const int bh = static_cast<int>(block / nblk);
-  const int64_t r0 = (block % nblk) * 32;
+  const int bh = static_cast<int>(blockIdx.x / nblk);
+  const int64_t r0 = (blockIdx.x % nblk) * 32;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const float4* acc = reinterpret_cast<const float4*>(p.dq_acc);
   // streaming (evict-first) loads and stores: the accumulator is dead after
@@ -187,11 +187,6 @@ __device__ __forceinline__ void dq_convert_block(const BwdParams& p, unsigned bl
     __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.dq) + (static_cast<size_t>(tok0 + r) * p.H + h) * D +
                                     8 * c), o);
   }
-}
-
-template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const BwdParams p) {
-  dq_convert_block<D>(p, blockIdx.x);
 }
 
 // ------------------------------------------------------------------ main kernel

@@ -69,7 +69,7 @@ struct ModBwdParams {
   float* dk_part;       // fp32 [B, N, Hv, d] partial dK (unscaled) and dV when a
   float* dv_part;       // group's heads are split, else nullptr
   float* dq_acc;        // layout: dq_acc_index4(); nullptr: dQ has a pass of its own
-  void* dq;             // written by that pass
+  void* dq;             // written by that pass or the conversion
   float* dvec;          // fp32 D [B, H, N]
   PlanView plan;
   int B, N, H, Hkv, G;
@@ -796,11 +796,30 @@ __global__ void __launch_bounds__(512, 1)
 // of the group's partial sums, in the order of the heads; one thread per four
 // columns, first the keys, then the values.
 template <int D>
-__global__ void __launch_bounds__(256) fa_mod_bwd_finish_kernel(const ModBwdParams p, const BwdParams conv,
-                                                               unsigned nconv, unsigned nred) {
+__global__ void __launch_bounds__(256) fa_mod_bwd_finish_kernel(const ModBwdParams p, unsigned nconv, unsigned nred) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel has ended and its sums are visible
-  if (blockIdx.x < nconv) {
-    dq_convert_block<D>(conv, blockIdx.x);
+  if (blockIdx.x < nconv) {  // 32 rows of one head, through shared memory as in fa_bwd_dq_convert_kernel
+    constexpr int G4 = D / 4, CPR = D / 8;
+    __shared__ float4 tile[32][G4 + 1];
+    const unsigned nblk = (static_cast<unsigned>(p.N) + 31u) / 32u;
+    const int bh = static_cast<int>(blockIdx.x / nblk), r0 = static_cast<int>(blockIdx.x % nblk) * 32;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const float4* acc = reinterpret_cast<const float4*>(p.dq_acc);
+#pragma unroll
+    for (int g = w; g < G4; g += 8)
+      if (r0 + lane < p.N) tile[lane][g] = __ldcs(acc + dq_acc_index4(bh, g, r0 + lane, p.N, D));
+    __syncthreads();
+    const int h = bh % p.H, b = bh / p.H;
+    uint4* dst = reinterpret_cast<uint4*>(p.dq) + ((static_cast<size_t>(b) * p.N + r0) * p.H + h) * CPR;
+#pragma unroll
+    for (int e = threadIdx.x; e < 32 * CPR; e += 256) {
+      const int r = e / CPR, c = e % CPR;
+      if (r0 + r >= p.N) continue;
+      const float4 x = tile[r][2 * c], y = tile[r][2 * c + 1];
+      __stcs(dst + static_cast<size_t>(r) * p.H * CPR + c,
+             make_uint4(pack_bf16x2(x.x * p.scale, x.y * p.scale), pack_bf16x2(x.z * p.scale, x.w * p.scale),
+                        pack_bf16x2(y.x * p.scale, y.y * p.scale), pack_bf16x2(y.z * p.scale, y.w * p.scale)));
+    }
     return;
   }
   const int64_t n4 = static_cast<int64_t>(p.B) * p.N * p.Hkv * (D / 4);
