@@ -9,6 +9,7 @@ include/fa.h for the definitions, layouts and limits.
 from __future__ import annotations
 
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -83,6 +84,25 @@ def mask_plan(B: int, N: int, causal: bool = False, window: int = 0, doc_ids: Op
     return MaskPlan(data, B, N)
 
 
+@lru_cache(maxsize=256)
+def _plan_size(B: int, N: int) -> int:
+    return int(lib().fa_mask_plan_size(B, N))
+
+
+def _need_plan(plan, B: int, N: int):
+    """`plan` must be mask_plan's for this B and N: the kernels index its bytes from
+    the sizes of q."""
+    if not isinstance(plan, MaskPlan):
+        raise TypeError("plan must come from mask_plan")
+    if (plan.B, plan.N) != (B, N):
+        raise ValueError(f"the plan is for B = {plan.B}, N = {plan.N}, not for B = {B}, N = {N}")
+    need = _plan_size(B, N)
+    t = plan.data
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.dim() == 1 and t.is_contiguous()
+            and t.shape[0] >= need):
+        raise ValueError(f"the plan's data must be the bytes that mask_plan wrote: contiguous uint8 of {need} or more")
+
+
 def _sizes(q, k, v, plan):
     _need(q, "q", torch.bfloat16, 4)
     _need(k, "k", torch.bfloat16, 4)
@@ -91,10 +111,7 @@ def _sizes(q, k, v, plan):
     if k.shape != (B, N, Hkv, d) or Hkv < 1 or H % Hkv != 0:
         raise ValueError(f"k must be [{B}, {N}, Hkv, {d}] with Hkv dividing {H}, got {tuple(k.shape)}")
     _need_shape(v, "v", torch.bfloat16, k.shape)
-    if not isinstance(plan, MaskPlan):
-        raise TypeError("plan must come from mask_plan")
-    if (plan.B, plan.N) != (B, N):
-        raise ValueError(f"the plan is for B = {plan.B}, N = {plan.N}, not for B = {B}, N = {N}")
+    _need_plan(plan, B, N)
     return B, N, H, Hkv, d
 
 

@@ -1,0 +1,70 @@
+"""Modified scores over the documented range of their arguments: explicit scales,
+slopes of any size, plans that do not hold what they claim, forward-mode
+derivatives, schedules of many short sequences, and decoding with each of them.
+
+Helpers and bounds are those of test_modified.py and test_cache.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_95_b200 as fa
+from exact_io_aware_95_b200 import build as fabuild
+from oracle import modified as om
+from tests.common import f64, rel_fro
+from tests.test_cache import check_decode, filled, query
+from tests.test_modified import FRO, MASKS, U, bf, bounds, cpu_plan, make, plan_of, see_of, slopes_of
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    fabuild.build()
+
+
+def against(x, mask, see, scale, softcap=0.0, slopes=None, oracle_slopes=None, elements=True, extra=0.0, least=0.0):
+    """The kernels under `mask` and `slopes` against the oracle over the pairs `see`
+    with `oracle_slopes`: element by element within bounds(), and (where an error
+    relative to the whole means something) in the Frobenius norm, with `extra` on its bar.
+    `least`: absolute bound of one rounding of a result, where it is more than relative ones."""
+    B, N, H, d = x["q"].shape
+    g = {n: t.cuda() for n, t in x.items()}
+    plan = plan_of(mask, B, N)
+    how = {"softcap": softcap, "slopes": None if slopes is None else slopes.cuda(), "scale": scale}
+    o, lse, low = fa.mod_fwd(g["q"], g["k"], g["v"], plan, low=True, **how)
+    grads = fa.mod_bwd(g["q"], g["k"], g["v"], o, lse, g["do"], plan, o_low=low, **how)
+    det = fa.mod_bwd(g["q"], g["k"], g["v"], o, lse, g["do"], plan, o_low=low, deterministic=True, **how)
+    fa.check_device_error()
+    osl = None if oracle_slopes is None else oracle_slopes.double().numpy()
+    a = [f64(x[n]) for n in ("q", "k", "v")]
+    want = {}
+    want["o"], L = om.mod_attn_fwd(*a, see, scale, softcap, osl)
+    want["dq"], want["dk"], want["dv"] = om.mod_attn_bwd(*a, f64(x["do"]), see, scale, softcap, osl)
+    tol = bounds(x, see, scale, softcap, osl)
+    l64 = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(l64), np.isneginf(L)) and not np.isnan(l64).any()
+    fin = np.isfinite(L)
+    if elements:
+        assert np.all(np.abs(l64[fin] - L[fin]) <= tol["lse"][fin])
+    got = dict(zip(("o", "dq", "dk", "dv"), (f64(t) for t in (o, *grads))))
+    for name, t in [*got.items(), ("dq", f64(det[0])), ("dk", f64(det[1])), ("dv", f64(det[2]))]:
+        assert np.isfinite(t).all(), name
+        if elements:
+            over = np.abs(t - want[name]) - tol[name] - least
+            assert over.max() <= 0, (name, over.max())
+        if np.linalg.norm(want[name]) > 1e-3 * np.linalg.norm(tol[name]) / U:
+            assert rel_fro(t, want[name]) <= FRO[name] + extra, name
+
+
+# ------------------------------------------------------------------ the plan
+def test_a_plan_of_other_bytes_is_refused():
+    q, k, lse = bf(2, 64, 4, 64), bf(2, 64, 2, 64), torch.zeros(2, 4, 64)
+    data = cpu_plan(2, 64).data
+    for bad in (data[:-1], data[:0], torch.zeros(1, dtype=torch.uint8), data.to(torch.int32), data.view(2, -1),
+                data.repeat_interleave(2)[::2], data.tolist(), None):
+        plan = fa.MaskPlan(bad, 2, 64)
+        for call in (lambda: fa.mod_fwd(q, k, k, plan), lambda: fa.mod_bwd(q, k, k, q, lse, q, plan),
+                     lambda: fa.mod_attention(q, k, k, plan),
+                     lambda: fa.mod_attention(q.clone().requires_grad_(True), k, k, plan)):
+            with pytest.raises((ValueError, TypeError), match="plan"):
+                call()
