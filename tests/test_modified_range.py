@@ -68,3 +68,42 @@ def test_a_plan_of_other_bytes_is_refused():
                      lambda: fa.mod_attention(q.clone().requires_grad_(True), k, k, plan)):
             with pytest.raises((ValueError, TypeError), match="plan"):
                 call()
+
+
+# ------------------------------------------------------------------ derivatives that it lacks
+def test_forward_mode_is_refused(monkeypatch):
+    """A dual tensor asks for no gradient in the reverse sense; its tangent must not
+    get lost silently."""
+    import torch.autograd.forward_ad as fwad
+    from exact_io_aware_95_b200 import modified
+    monkeypatch.setattr(modified, "mod_fwd", lambda q, k, v, plan, **kw: tuple(q.clone() for _ in range(2 + kw.get("low", False))))
+    q, k, plan = bf(1, 8, 2, 64), bf(1, 8, 1, 64), cpu_plan(1, 8)
+    with fwad.dual_level():
+        for i in range(3):
+            args = [q, k, k]
+            args[i] = fwad.make_dual(args[i], torch.ones_like(args[i]))
+            with pytest.raises(RuntimeError):
+                fa.mod_attention(*args, plan)
+    assert not fa.mod_attention(q, k, k, plan).requires_grad
+    with torch.no_grad():
+        assert not fa.mod_attention(q.clone().requires_grad_(True), k, k, plan).requires_grad
+
+
+def test_what_rounding_lost_is_kept_for_a_backward_only(monkeypatch):
+    """mod_attention asks mod_fwd for the residual of O when a gradient may follow."""
+    from exact_io_aware_95_b200 import modified
+    asked = []
+
+    def fake(q, k, v, plan, **kw):
+        asked.append(bool(kw.get("low")))
+        return tuple(q.clone() for _ in range(2 + bool(kw.get("low"))))
+
+    monkeypatch.setattr(modified, "mod_fwd", fake)
+    q, k, plan = bf(1, 8, 2, 64), bf(1, 8, 1, 64), cpu_plan(1, 8)
+    leaf = q.clone().requires_grad_(True)
+    fa.mod_attention(q, k, k, plan)
+    fa.mod_attention(leaf, k, k, plan)
+    fa.mod_attention(q, k, k.clone().requires_grad_(True), plan)
+    with torch.no_grad():
+        fa.mod_attention(leaf, k, k, plan)
+    assert asked == [False, True, True, False]
