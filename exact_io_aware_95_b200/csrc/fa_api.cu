@@ -997,9 +997,17 @@ fa_status fa_mod_fwd(const void* q, const void* k, const void* v, void* o, void*
   p.scale_log2 = scale * kLog2e;
   p.x_mul = softcap > 0.f ? scale / softcap : 0.f;
   p.cap_log2 = softcap * kLog2e;
+  bool cap = softcap > 0.f;
+  if (scale == 0.f && !cap && !slopes) {
+    // The variant without cap and bias multiplies by the scale after the mask, where
+    // 0 would turn a masked score's -inf into NaN.  Any cap leaves scores of 0 as
+    // they are, and the capped variant scales before it masks: x_mul = 0, cap 1.
+    cap = true;
+    p.cap_log2 = kLog2e;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d == 64 ? dispatch_mod_fwd<64>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, p, s)
-                 : dispatch_mod_fwd<128>(dev, softcap > 0.f, slopes != nullptr, mq, mk, mv, p, s);
+  return d == 64 ? dispatch_mod_fwd<64>(dev, cap, slopes != nullptr, mq, mk, mv, p, s)
+                 : dispatch_mod_fwd<128>(dev, cap, slopes != nullptr, mq, mk, mv, p, s);
 }
 
 size_t fa_mod_bwd_workspace_size(int B, int N, int H, int Hkv, int d) {
