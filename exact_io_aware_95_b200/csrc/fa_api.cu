@@ -508,13 +508,14 @@ bool valid_plan_shape(int B, int N) {
   return B >= 1 && B <= 65535 && N >= 1 && N <= (1 << 24) && static_cast<int64_t>(B) * N <= 0x7fffffff;
 }
 
-// Scores: finite scale and cap, and scale / cap and cap * log2(e), by which the
-// kernels multiply, finite and not subnormal.
+// Scores: finite scale and cap; what the kernels multiply by finite too, scale *
+// log2(e) without a cap, with one (2 log2(e) times) scale / cap and cap, and these
+// two not subnormal.
 bool valid_cap(float scale, float softcap) {
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return false;
-  if (softcap == 0.f) return true;
+  if (softcap == 0.f) return std::isfinite(scale * kLog2e);
   const float x_mul = scale / softcap, cap = softcap * kLog2e;
-  return std::isfinite(x_mul) && std::isfinite(cap) && (scale == 0.f || std::isnormal(x_mul)) && std::isnormal(cap);
+  return std::isfinite(2.f * kLog2e * x_mul) && std::isfinite(2.f * cap) && (scale == 0.f || std::isnormal(x_mul)) && std::isnormal(cap);
 }
 
 // ------------------------------------------------- modified-score attention

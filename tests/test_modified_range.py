@@ -97,6 +97,23 @@ def test_decode_scales(softcap, bias, d):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), scale
 
 
+# ------------------------------------------------------------------ scales out of range
+def test_scales_out_of_range_are_refused():
+    """What the kernels multiply scores by has to be finite: scale log2(e), and with a
+    cap 2 log2(e) times scale / cap and cap."""
+    L, P, inv = fa.lib(), 4096, fa.FA_ERR_INVALID_ARG
+    f = [P, P, P, P, None, P, P, None]
+    b = [P] * 4 + [None] + [P] * 6 + [None, P]
+    c = [P] * 7 + [None, None, P]
+    ws, wc = L.fa_mod_bwd_workspace_size(1, 8, 2, 1, 64), L.fa_cache_decode_workspace_size(1, 1, 64, 2, 1, 64)
+    for scale, cap in ((3e38, 0.0), (float("inf"), 0.0), (float("nan"), 0.0), (2e38, 1.0), (1e30, 2e38)):
+        assert L.fa_mod_fwd(*f, 1, 8, 2, 1, 64, scale, cap, None) == inv
+        for call in (L.fa_mod_bwd, L.fa_mod_bwd_deterministic):
+            assert call(*b, ws, 1, 8, 2, 1, 64, scale, cap, None) == inv
+        for x in (scale, -scale):
+            assert L.fa_cache_decode_fwd(*c, wc, 1, 1, 64, 2, 1, 64, x, cap, 0, 0, None) == inv
+
+
 # ------------------------------------------------------------------ the plan
 def test_a_plan_of_other_bytes_is_refused():
     q, k, lse = bf(2, 64, 4, 64), bf(2, 64, 2, 64), torch.zeros(2, 4, 64)
