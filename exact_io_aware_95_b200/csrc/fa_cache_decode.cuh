@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
   constexpr int MT = D / 16;      // 16-dimension tiles of the output
   float* sMl = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* sAcc = reinterpret_cast<float*>(smem + C::OFF_ACC);
-  constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kLazy = 8.f;    // the maxima move when exceeded by more than 2^8
   const bool windowed = p.window > 0 && p.window < p.Nk;
   int gtile = 0;
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
       const int ea = a > 0.f ? max(static_cast<int>(__float_as_uint(a) >> 23) - 127 - 14, -120) : 0;
       const float mul = __uint_as_float(static_cast<uint32_t>(127 - ea) << 23);
       const float rf = (CAP ? p.x_mul : p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + ea) << 23);
-      const float sl = BIAS ? p.slopes[h] * kLog2e : 0.f;
+      const float sl = BIAS ? slope_log2(p.slopes[h]) : 0.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {  // k-step s: this thread's dimensions 4s .. 4s + 3
         qb[nb][s][0] = pack_h2(bf16lo_to_f32(x[2 * s]) * mul, bf16hi_to_f32(x[2 * s]) * mul);

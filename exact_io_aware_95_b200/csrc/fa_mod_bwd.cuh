@@ -30,7 +30,8 @@
 //     bits: relative error of dQ 5.2e-3 against 3.0e-3 at q = 8 N(0,1),
 //     k = N(0,1), d = 64, N = 1024;
 //   - the row term of the exponent, -LSE_i log2 e, carries the query's part of
-//     a one-sided distance bias (the key's part is one constant per thread);
+//     a one-sided distance bias (the key's part is one constant per thread), for
+//     slopes up to 4: see kSplitSlope;
 //   - between its two phases the thread keeps P (1 - t^2) 2^15 in fp16 for dS:
 //     one register per pair as with bf16(P), but with an error of 2^-11 instead
 //     of 2^-8 down to P = 2^-29 (below, 2^-40 absolute: less than the rounding
@@ -51,6 +52,13 @@
 
 namespace fa {
 
+// Steepest bias whose two parts, the query's and the key's, are rounded apart: both
+// reach 127 slope log2(e) where the distance may be 0, and four roundings of that size
+// put an error of at most 3.1e-5 slope (relative) into P: here 1.2e-4, a quarter of
+// the rounding of P to fp16.  Steeper ones take the exact distance element by element
+// (that of 3000 would lose 2% of the diagonal's P, that of 1e5 overflow it), at
+// 2 x 16 x 8192 x 64 with documents in 466 us where two parts take 441.
+constexpr float kSplitSlope = 4.f;
 constexpr float kDsUp = 32768.f;  // P <= 1 (and a rounding) times this stays finite in fp16
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -527,12 +535,13 @@ __global__ void __launch_bounds__(512, 1)
         named_bar_sync(1 + w, 128);  // the warpgroup is done with the previous tile's values
         const bool tile_full = k0 >= n_lo && k0 + 128 <= n_hi;
         // How the bias runs over the tile pair: below the diagonal (or no row
-        // sees past itself) +1, above it -1, both sides 0
+        // sees past itself) +1, above it -1, both sides (or a steep one) 0
         int tile_side = 0;
         float tile_slope = 0.f;
         if constexpr (BIAS) {
           tile_side = (q0 >= k0 + 127 || !n_ahead) ? 1 : (q0 + 127 <= k0 ? -1 : 0);
-          tile_slope = n_slope * kLog2e;
+          if (fabsf(n_slope) > kSplitSlope) tile_side = 0;
+          tile_slope = slope_log2(n_slope);
         }
         if (t < 64) {
           // -LSE in base 2, with the query's part of a one-sided bias

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(320, 1)
       dvl = -p.dvec[li] / kDsUp;
       see = p.plan.rows[static_cast<size_t>(b) * p.N + q];
     }
-    const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
+    const float slope = BIAS ? slope_log2(p.slopes[h]) : 0.f;
     const uint64_t y2 = CAP ? f2_pack(p.cap_log2, p.cap_log2) : f2_pack(p.scale_log2, p.scale_log2);
     const uint64_t up = f2_pack(kDsUp, kDsUp), down = f2_pack(-kDsUp, -kDsUp), dn = f2_pack(1.f / kDsUp, 1.f / kDsUp);
     const uint32_t region = sbase + C::OFF_DS + w * 16384;  // keys 64w..64w+63 of dS

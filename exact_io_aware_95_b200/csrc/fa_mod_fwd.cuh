@@ -83,6 +83,13 @@ __device__ __forceinline__ uint64_t tanh2_any(uint64_t x2, uint64_t base, uint64
   return ffma2(f2_pack(rcp_approx(a), rcp_approx(b)), mul, base);
 }
 
+// slope log2(e).  Kept finite, so that a distance of 0 adds 0 where the product
+// overflows (slopes beyond 2.36e38); NaN stays NaN.
+__device__ __forceinline__ float slope_log2(float slope) {
+  const float s = slope * 1.4426950408889634f;
+  return fabsf(s) == INFINITY ? copysignf(3.402823466e38f, s) : s;
+}
+
 struct ModFwdParams {
   void* o;
   void* o_low;          // bf16(O - bf16(O)), or nullptr
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(384, 1)
       int2 see = make_int2(0, 0);
       if (qi < p.N) see = p.plan.rows[static_cast<size_t>(I.b) * p.N + qi];
       float slope = 0.f;
-      if (BIAS) slope = p.slopes[I.h] * 1.4426950408889634f;
+      if (BIAS) slope = slope_log2(p.slopes[I.h]);
       // no key after the query is visible: the bias is one-sided on every tile
       const bool behind = see.y <= qi + 1;
       float m = -INFINITY;         // reference max, log2 units

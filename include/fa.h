@@ -182,7 +182,8 @@ fa_status fa_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
  *   - softcap > 0: the scores x = scale * q . k become
  *     softcap * tanh(x / softcap); 0 leaves them as they are;
  *   - slopes (fp32 [H] device array, or NULL): the score of query i and key j
- *     is then lowered by slopes[h] * |i - j| (any finite slope);
+ *     is then lowered by slopes[h] * |i - j|: any slope >= 0, or a negative one
+ *     with slopes[h] * log2(e) * |i - j| finite for the pairs seen;
  *   - the keys each query sees come from a mask plan, not from a flag.
  * scale is >= 0 here, and scale * log2(e) finite; with a cap, scale / softcap is a
  * normal number (or 0), and it and softcap stay finite times 2 log2(e).

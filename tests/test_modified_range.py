@@ -114,6 +114,67 @@ def test_scales_out_of_range_are_refused():
             assert L.fa_cache_decode_fwd(*c, wc, 1, 1, 64, 2, 1, 64, x, cap, 0, 0, None) == inv
 
 
+# ------------------------------------------------------------------ slopes
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix", "documents"])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("slope", [300.0, 3e3, 3e4, 1e6, 1e9, 3e38])
+def test_slopes_that_leave_one_key(slope, cap, mask, d):
+    """Scores here differ by less than 60, so any other key's weight is below e^-240,
+    which is 0 in fp32: the row attends to itself alone, with weight 1, and the
+    oracle of that is the attention over the diagonal."""
+    B, N, H, Hkv = 2, 201, 2, 1
+    m = MASKS[mask](B, N)
+    see = see_of(m, B, N) & np.eye(N, dtype=bool)
+    x = make(B, N, H, Hkv, d, 45)
+    q, k = f64(x["q"]), np.repeat(f64(x["k"]), H // Hkv, 2)
+    scores = np.einsum("bihc,bjhc->bhij", q, k) / math.sqrt(d)
+    assert np.abs(scores).max() < 30
+    against(x, m, see, 1 / math.sqrt(d), cap, torch.full((H,), slope))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix", "documents_both"])
+@pytest.mark.parametrize("slope", [3.9, 4.1, 20.0])
+def test_steep_slopes(slope, mask):
+    """On both sides of the size from which the backward pass takes the distance
+    element by element; large scores, so that several keys of a row count."""
+    B, N, H = 2, 260, 2
+    m, sl = MASKS[mask](B, N), torch.tensor([slope, slope / 2])
+    against(make(B, N, H, 1, 64, 46, gain=20.0), m, see_of(m, B, N), 1 / 8, 0.0, sl, sl)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix"])
+def test_steep_negative_slopes(mask):
+    """Far keys win, and the scores reach 260 x 20 = 5200, 7503 in base 2: below 2^13,
+    so a rounding of one is off by at most 2^-11, 3.4e-4 of a weight.  The recomputed
+    P has four of them (the forward's logsumexp, half of whose last place is 2^-12,
+    and its product with log2 e; the bias; the sum), 1.3e-3, and the forward's weights
+    two, 7e-4: 2e-3 on the bar.  Elements have no bound of bounds(), which takes
+    the bias as positive."""
+    B, N, H = 2, 260, 2
+    m, sl = MASKS[mask](B, N), torch.tensor([-20.0, -5.0])
+    against(make(B, N, H, 1, 64, 47), m, see_of(m, B, N), 1 / 8, 0.0, sl, sl, elements=False, extra=2e-3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("slope", [3e3, 1e9, 3e38])
+def test_decode_slopes_that_leave_one_key(slope):
+    """Each query sees its own key alone (see above): O is that key's value."""
+    c = filled(3, 150, 1, 64, 48)
+    lens = torch.tensor([150, 64, 3], dtype=torch.int32)
+    q = query(3, 2, 2, 64, 49)
+    for cap in (0.0, 20.0):
+        o, lse = fa.cache_decode_fwd(q.cuda(), c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"], lens.cuda(),
+                                     causal=True, softcap=cap, slopes=torch.full((2,), slope).cuda())
+        v = fa.cache_read(c["v_cache"], c["v_scale"])
+        for b in range(3):
+            for i in range(2):
+                assert torch.equal(o[b, i], v[b, int(lens[b]) - 2 + i].expand(2, 64)) and torch.isfinite(lse).all()
+
+
 # ------------------------------------------------------------------ the plan
 def test_a_plan_of_other_bytes_is_refused():
     q, k, lse = bf(2, 64, 4, 64), bf(2, 64, 2, 64), torch.zeros(2, 4, 64)
