@@ -466,7 +466,17 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           for (int e = 0; e < 2; ++e)
             z2[nb][e] = fmul2(f2_pack(sc[nb][2 * e], sc[nb][2 * e + 1]),
                               f2_pack(rowf[2 * nb] * ks[e], rowf[2 * nb + 1] * ks[e]));
+        const bool edge = k0 + 16 > L || k0 < key_lo;  // warp-uniform: some key here is no query's
         if constexpr (CAP) {
+          if (edge) {  // such a key has no part in the choice below: it may hold anything
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = k0 + g + 8 * e;
+              if (key >= L || key < key_lo)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) z2[nb][e] = 0;
+            }
+          }
           // the polynomial within its range: the exponential form's error is
           // 6e-8 of the cap even where the scores are small
           float ax = 0.f;
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           wb[nb][1] = movmatrix_trans(pack_h2(ex2(so[nb][2] - nmo[0]), ex2(so[nb][3] - nmo[1])));
         }
         // ---- output
-        if (k0 + 16 > L || k0 < key_lo) {  // rows no query sees may hold NaN codes: 0 x NaN
+        if (edge) {  // rows no query sees may hold NaN codes: 0 x NaN
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = k0 + 2 * t + (i & 1) + 8 * (i >> 1);

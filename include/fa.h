@@ -187,6 +187,9 @@ fa_status fa_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
  *   - the keys each query sees come from a mask plan, not from a flag.
  * scale is >= 0 here, and scale * log2(e) finite; with a cap, scale / softcap is a
  * normal number (or 0), and it and softcap stay finite times 2 log2(e).
+ * With a cap, the tanh of a block of scores takes one of two forms (both within
+ * 1e-7), by the block's largest: the last bits of a row may depend on the rows and
+ * keys beside it, masked ones among them.
  * A query that sees no key gets O = 0, LSE = -inf and no gradient; a key that
  * no query sees gets dK = dV = 0.  K and V must be finite also in rows that
  * are masked (padding): they enter products with weight 0. */
@@ -270,7 +273,7 @@ fa_status fa_cache_read(const void* cache, const void* scale, const int* seqlens
  * fa_mod_fwd, with |position - j| as the distance; causal = 1: keys
  * j <= position; window > 0: keys |position - j| < window.  A query that sees
  * no key gets O = 0, LSE = -inf.  Rows that no query of the entry sees may hold
- * anything.  scale may have either sign; otherwise its limits are fa_mod_fwd's.
+ * anything, without a change of a bit.  scale may have either sign; otherwise its limits are fa_mod_fwd's.
  * Lengths outside [0, Nk] and errors as in fa_decode_fwd.
  * workspace: ws_bytes >= fa_cache_decode_workspace_size(), 256-byte aligned (it
  * depends on Hkv and d only); calls that may run at the same time, captured ones

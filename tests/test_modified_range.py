@@ -226,3 +226,26 @@ def test_what_rounding_lost_is_kept_for_a_backward_only(monkeypatch):
     with torch.no_grad():
         fa.mod_attention(leaf, k, k, plan)
     assert asked == [False, True, True, False]
+
+
+# ------------------------------------------------------------------ decoding
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 50])
+def test_capped_decode_ignores_rows_no_query_sees(window, d):
+    """Rows past the length and before the window hold zeros, or large finite values
+    whose scores are far beyond the cap: the same bits."""
+    c = filled(3, 333, 2, d, 51)
+    lens = torch.tensor([333, 100, 7], dtype=torch.int32)
+    for Nq in (1, 5):
+        q = query(3, Nq, 4, d, 52)
+        outs = []
+        for code, exp in ((0x00, 127), (0x7e, 160)):  # 0; 448 2^33
+            held = {n: t.clone() for n, t in c.items()}
+            for b, L in enumerate(lens.tolist()):
+                for part in (slice(L, None), slice(0, max(0, L - Nq + 1 - window) if window else 0)):
+                    for n in ("k", "v"):
+                        held[n + "_cache"].view(torch.uint8)[b, part] = code
+                        held[n + "_scale"][b, :, part] = exp
+            outs.append(check_decode(q, held, lens, softcap=30.0, window=window))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
