@@ -696,12 +696,14 @@ fa_status mod_bwd_common(const void* q, const void* k, const void* v, const void
 
 // ------------------------------------------------------------- 8-bit cache
 // A block's share of (token, head) rows: about 64 rows of whole tokens, or one
-// token's heads 256 at a time (measured on 8 x 2047 x 8 x 128: 32 rows 23.7 us,
+// token's heads kCacheRows at a time (measured on 8 x 2047 x 8 x 128: 32 rows 23.7 us,
 // 64 rows 21.7, 256 rows 24.8).
 template <typename P>
 void cache_chunks(P& p, int Hkv) {
-  p.tb = Hkv >= 64 ? 1 : 64 / Hkv;
-  p.hb = Hkv > 256 ? 256 : Hkv;
+  constexpr int kTokenRows = 64;
+  static_assert(kTokenRows <= fa::kCacheRows, "a block's rows fit its shared memory");
+  p.tb = Hkv >= kTokenRows ? 1 : kTokenRows / Hkv;  // tb Hkv <= kTokenRows, or one token
+  p.hb = std::min(Hkv, fa::kCacheRows);
   p.hchunks = (Hkv + p.hb - 1) / p.hb;
 }
 

@@ -80,7 +80,7 @@ struct CacheAppendParams {
 // on leave for a slow path, voted on by warp; the exponent bytes are collected
 // in shared memory and written head by head.  8 x 2047 x 8 x 128 (half to all of
 // it valid): 21.6 -> 16.5 us.
-constexpr int kCacheRows = 512;  // rows (token, head) of a block at most
+constexpr int kCacheRows = 256;  // rows (token, head) of a block at most; the host's split keeps to it
 
 template <int D>
 __global__ void __launch_bounds__(256) fa_cache_append_kernel(const CacheAppendParams p) {

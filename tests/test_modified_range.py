@@ -13,7 +13,7 @@ import exact_io_aware_95_b200 as fa
 from exact_io_aware_95_b200 import build as fabuild
 from oracle import modified as om
 from tests.common import f64, rel_fro
-from tests.test_cache import check_decode, filled, query
+from tests.test_cache import check_decode, empty_cache, filled, query
 from tests.test_modified import FRO, MASKS, U, bf, bounds, cpu_plan, make, plan_of, see_of, slopes_of
 
 
@@ -249,3 +249,25 @@ def test_capped_decode_ignores_rows_no_query_sees(window, d):
                         held[n + "_scale"][b, :, part] = exp
             outs.append(check_decode(q, held, lens, softcap=30.0, window=window))
         assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# ------------------------------------------------------------------ cache blocks
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hkv", [1, 63, 64, 65, 255, 256, 257, 513])
+def test_cache_rows_around_a_block(Hkv):
+    """Head counts around those where a block's share of rows changes: values that
+    e4m3 holds exactly come back as they went in."""
+    B, T, d = 2, 3, 64
+    g = torch.Generator().manual_seed(53)
+    x = torch.randint(-8, 9, (2, B, T, Hkv, d), generator=g) * torch.exp2(torch.randint(-20, 20, (2, B, T, Hkv, 1), generator=g).float())
+    x = x.bfloat16().cuda()
+    c = empty_cache(B, T + 4, Hkv, d)
+    before = {n: t.clone() for n, t in c.items()}
+    fa.cache_append(x[0], x[1], c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"],
+                    torch.tensor([1, 4], dtype=torch.int32).cuda())
+    for i, n in enumerate("kv"):
+        out = fa.cache_read(c[n + "_cache"], c[n + "_scale"])
+        old = fa.cache_read(before[n + "_cache"], before[n + "_scale"])
+        old[0, 1:4], old[1, 4:7] = x[i, 0], x[i, 1]
+        assert torch.equal(out, old)
+    fa.check_device_error()
