@@ -228,6 +228,38 @@ def test_what_rounding_lost_is_kept_for_a_backward_only(monkeypatch):
     assert asked == [False, True, True, False]
 
 
+# ------------------------------------------------------------------ schedules
+@pytest.mark.gpu
+def test_backward_items_in_groups():
+    """More than 4096 items of the backward pass go in groups of heads whose rows fit
+    the L2 cache, the last group shorter than the others: the same gradients as in
+    calls of one group.  Each dQ row has two terms, so their order does not show."""
+    B, N, H, d, part = 300, 130, 7, 64, 50
+    group = (48 << 20) // (N * d * 8)
+    assert B * H * 2 > 4096 and group < B * H and (B * H) % group and part * H * 2 <= 4096
+    g = torch.Generator(device="cuda").manual_seed(50)
+    q, k, v, do = (torch.randn(B, N, H, d, generator=g, device="cuda").bfloat16() for _ in range(4))
+    how = {"softcap": 20.0, "slopes": slopes_of(H).cuda()}
+
+    def step(x):
+        plan = fa.mask_plan(len(x[0]), N, causal=True, device="cuda")
+        o, lse, low = fa.mod_fwd(*x[:3], plan, low=True, **how)
+        outs = [torch.full_like(t, float("nan")) for t in x[:3]]
+        fa.mod_bwd(*x[:3], o, lse, x[3], plan, o_low=low, dq=outs[0], dk=outs[1], dv=outs[2], **how)
+        return o, lse, *outs
+
+    whole = step((q, k, v, do))
+    for b in range(0, B, part):
+        for a, c in zip(step(tuple(t[b:b + part] for t in (q, k, v, do))), whole):
+            assert torch.equal(a, c[b:b + part])
+    x = {n: t[-2:].cpu() for n, t in zip(("q", "k", "v", "do"), (q, k, v, do))}  # of the last group
+    see = see_of({"causal": True}, 2, N)
+    tol = bounds(x, see, 1 / 8, 20.0, how["slopes"].double().cpu().numpy())
+    want = om.mod_attn_bwd(*(f64(x[n]) for n in ("q", "k", "v", "do")), see, 1 / 8, 20.0, how["slopes"].double().cpu().numpy())
+    for n, t, w in zip(("dq", "dk", "dv"), whole[2:], want):
+        assert (np.abs(f64(t[-2:]) - w) - tol[n]).max() <= 0, n
+
+
 # ------------------------------------------------------------------ decoding
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
