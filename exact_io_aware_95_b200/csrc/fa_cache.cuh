@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t pack_e4m3x2_sat(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// 2^(e - 127) for an exponent byte (E8M0: 255 is NaN, 0 is 2^-127)
+// 2^(e - 127) for an exponent byte (E8M0: 255 is NaN, 0 is 2^-127); -0 for 256
 __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7fffffffu : (e == 0u ? 0x00400000u : e << 23));
 }

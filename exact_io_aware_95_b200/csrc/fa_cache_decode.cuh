@@ -376,20 +376,34 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) acc[i][nb][0] = acc[i][nb][1] = acc[i][nb][2] = acc[i][nb][3] = 0.f;
 
-    // exponent bytes of this thread's keys g, g + 8 (keys, values), fetched one tile ahead
+    // keys [key_lo, L) are those that some query of the entry sees
+    const int key_lo = windowed ? max(0, L - p.Nq - p.window + 1) : 0;
+    // exponent bytes of this thread's keys g, g + 8 (keys, values), fetched one tile
+    // ahead.  With a cap, a key no query sees gets a key scale of (minus) 0, whatever it
+    // holds: its score is 0 where the form of the tanh is chosen.  (Zeroing the scores
+    // there instead, or two comparisons a key here, costs 1 to 2% of a capped call.)
     const size_t plane = (static_cast<size_t>(w.b) * p.Hkv + hk) * p.Nk + warp * 16 + g;
     const uint8_t *ke = p.kexp + plane, *ve = p.vexp + plane;
+    const uint32_t span = static_cast<uint32_t>(L - key_lo);
     uint32_t ex[4];
     auto fetch_exp = [&](int tile) {
-      const int k = tile * C::KT, left = L - warp * 16 - g - k;
-      ex[0] = left > 0 ? ke[k] : 127u;
-      ex[1] = left > 8 ? ke[k + 8] : 127u;
-      ex[2] = left > 0 ? ve[k] : 127u;
-      ex[3] = left > 8 ? ve[k + 8] : 127u;
+      const int k = tile * C::KT;
+      if constexpr (CAP) {
+        const uint32_t at = static_cast<uint32_t>(k + warp * 16 + g - key_lo);
+        ex[0] = at < span ? ke[k] : 256u;  // e8m0_value: -0
+        ex[1] = at + 8u < span ? ke[k + 8] : 256u;
+        ex[2] = at < span ? ve[k] : 127u;
+        ex[3] = at + 8u < span ? ve[k + 8] : 127u;
+      } else {
+        const int left = L - warp * 16 - g - k;
+        ex[0] = left > 0 ? ke[k] : 127u;
+        ex[1] = left > 8 ? ke[k + 8] : 127u;
+        ex[2] = left > 0 ? ve[k] : 127u;
+        ex[3] = left > 8 ? ve[k + 8] : 127u;
+      }
     };
     fetch_exp(w.tp);
-    // keys that some query of the entry sees, and keys that all of them see
-    const int key_lo = windowed ? L - p.Nq - p.window + 1 : 0;
+    // keys that all queries of the entry see
     const int full_lo = windowed ? L - p.window : 0;
     const int full_hi = min(p.causal ? L - p.Nq + 1 : L, windowed ? L - p.Nq + p.window : L);
     bool ok = true;
@@ -466,17 +480,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           for (int e = 0; e < 2; ++e)
             z2[nb][e] = fmul2(f2_pack(sc[nb][2 * e], sc[nb][2 * e + 1]),
                               f2_pack(rowf[2 * nb] * ks[e], rowf[2 * nb + 1] * ks[e]));
-        const bool edge = k0 + 16 > L || k0 < key_lo;  // warp-uniform: some key here is no query's
         if constexpr (CAP) {
-          if (edge) {  // such a key has no part in the choice below: it may hold anything
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = k0 + g + 8 * e;
-              if (key >= L || key < key_lo)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) z2[nb][e] = 0;
-            }
-          }
           // the polynomial within its range: the exponential form's error is
           // 6e-8 of the cap even where the scores are small
           float ax = 0.f;
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(160, cdec_ctas_per_sm(NB))
           wb[nb][1] = movmatrix_trans(pack_h2(ex2(so[nb][2] - nmo[0]), ex2(so[nb][3] - nmo[1])));
         }
         // ---- output
-        if (edge) {  // rows no query sees may hold NaN codes: 0 x NaN
+        if (k0 + 16 > L || k0 < key_lo) {  // rows no query sees may hold NaN codes: 0 x NaN
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = k0 + 2 * t + (i & 1) + 8 * (i >> 1);
