@@ -303,3 +303,45 @@ def test_cache_rows_around_a_block(Hkv):
         old[0, 1:4], old[1, 4:7] = x[i, 0], x[i, 1]
         assert torch.equal(out, old)
     fa.check_device_error()
+
+
+# ------------------------------------------------------------------ infinities
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_scores_under_a_cap(d):
+    """tanh(inf) = 1: a capped score of an infinite product is the cap, as it is of one
+    far beyond it (e^(2x) is infinite in both); masked ones stay out."""
+    cap, m = 2.0, {"causal": True}
+    x = make(1, 200, 2, 1, d, 54)
+    plan = plan_of(m, 1, 200)
+    outs = []
+    for big in (float("inf"), 1e30):
+        y = {n: t.clone() for n, t in x.items()}
+        y["q"][0, 50, 1, 3], y["q"][0, 150, 0, 7] = big, -big
+        y["k"][0, 70, 0, 5], y["k"][0, 130, 0, 1] = big, -big
+        # every score that meets two of them is a sum of infinities of either sign
+        o, lse = fa.mod_fwd(*(y[n].cuda() for n in ("q", "k", "v")), plan, softcap=cap)
+        outs.append((f64(o), lse.double().cpu().numpy()))
+    O, L = om.mod_attn_fwd(f64(y["q"]), f64(y["k"]), f64(x["v"]), see_of(m, 1, 200), 1 / math.sqrt(d), cap)
+    rows = np.ones((1, 200, 2), bool)
+    rows[0, 150, 0] = False  # row 150 of head 0 sees both infinite keys, with an infinite query
+    fin = rows.transpose(0, 2, 1)
+    assert np.array_equal(outs[0][0][rows], outs[1][0][rows]) and np.array_equal(outs[0][1][fin], outs[1][1][fin])
+    # weights rounded to bf16 (2 U of the sum of p |v|) and O (U); the products' sums: d 2^-24
+    # of scale sum |q k|, which is below 12 where it is finite
+    assert (np.abs(outs[0][0] - O)[rows] <= 4 * U * np.abs(f64(x["v"])).max()).all()
+    assert (np.abs(outs[0][1] - L)[fin] <= 2.0 ** -13).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bias", [False, True])
+def test_an_infinite_query_stays_in_its_row(bias):
+    x = make(1, 200, 2, 1, 64, 55)
+    sl = slopes_of(2).cuda() if bias else None
+    plan = plan_of({"causal": True}, 1, 200)
+    want = fa.mod_fwd(*(x[n].cuda() for n in ("q", "k", "v")), plan, slopes=sl)
+    x["q"][0, 60, 1, 3] = float("inf")
+    o, lse = fa.mod_fwd(*(x[n].cuda() for n in ("q", "k", "v")), plan, slopes=sl)
+    assert not torch.isfinite(lse[0, 1, 60])  # +inf where the products have one sign, NaN else
+    o[0, 60, 1], lse[0, 1, 60] = want[0][0, 60, 1], want[1][0, 1, 60]
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
