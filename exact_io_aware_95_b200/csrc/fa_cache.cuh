@@ -15,10 +15,10 @@
 // Caches are [B, Nk, Hkv, d] bytes, exponents [B, Hkv, Nk] so that the keys of
 // one head are contiguous where the decoding kernel streams them.
 //
-// Both kernels are bound by HBM (append: 2d read, d + 1 written per row; read:
-// d + 1 read, 2d written): 8 x 2047 x 8 x 128 appended in 16.5 us (76 MB: 0.70 of
-// the copy bandwidth, launch and ramp included), 8 x 8191 x 8 x 128 half full read
-// in 29.6 us (168 MB: 0.87).
+// Reading is bound by HBM (d + 1 bytes read and 2d written per row): 8 x 8191 x 8 x
+// 128 half full in 28.4-29.6 us (168 MB: 0.87-0.90 of the copy bandwidth).  Appending
+// (2d read, d + 1 written) is bound by instruction issue as much: 8 x 2047 x 8 x 128
+// in 16.7 us of device time (76 MB: 0.69), 72% of the issue slots busy.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -20,7 +20,8 @@
 //     under 2^15 and is then exact in fp16 down to 2^-24 (its 8 significant
 //     bits fit); row scale and key scale are applied to the fp32 score.
 //   - The weight of key j in the second product is w_ij = 2^(z_ij + ev_j - mo_i)
-//     in fp16 (error 2^-11 relative, an eighth of the output's rounding to bf16):
+//     in fp16 (error 2^-11 relative, an eighth of the output's rounding to bf16; half
+//     a step of 2^-24 where the weight is below 2^-14 of the one that set mo_i):
 //     the value row's exponent ev_j joins the weight's, with a running maximum
 //     mo_i of its own, so the largest contribution keeps full precision whatever
 //     the spread of the value scales.  The row sum is taken of 2^(z_ij - m_i)
@@ -47,11 +48,16 @@
 // merged through their logsumexps by a second kernel.  Each CTA finds its chunk
 // by scanning the lengths itself: no prefix launch.
 //
-// Measured: 16 x 16(16) x 16384 x 128 full 176-190 us (1.08 GB: 0.87-0.94 of the
-// copy bandwidth), 64 x 32(8) x 8192 x 128 ragged and capped 107 us (0.54 GB: 0.77;
-// the rest is the start, the piece ends and the merge), one 100-row cache 7 us,
-// which is the latency of two launches.  ncu: DRAM bytes equal the algorithmic
-// ones, issue slots 50% busy, tensor pipe 17%.
+// Measured, a call among others: 16 x 16(16) x 16384 x 128 full 190-205 us (1.08 GB:
+// 0.81-0.87 of the copy bandwidth; the stream kernel alone 174 us under ncu),
+// 64 x 32(8) x 8192 x 128 ragged and capped 109-121 us by the lengths drawn (0.54 GB
+// on average: 0.68-0.76; the rest is the start, the piece ends and the merge), one
+// 100-row cache 7 + 3 us on the device.  ncu: DRAM bytes within 3% of the algorithmic
+// ones, issue slots 49% busy, tensor pipe 16%.
+// More than 16 query rows read the cache again, 16 at a time, and at d = 128 the 168
+// registers of NB = 2 do not hold queries, accumulators and values (280 to 360 bytes
+// spilled): 16 sequences x 8 key heads x 16384 x 128, floor 83 us, take 102 us with 8
+// rows per key head, 174 with 16, 326 with 32, 1197 with 128.
 #pragma once
 #include "fa_cache.cuh"
 #include "fa_mod_fwd.cuh"

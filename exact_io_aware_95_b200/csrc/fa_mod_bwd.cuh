@@ -40,8 +40,10 @@
 //
 // Bound like the plain backward (shared-memory operands, the P and dS chain):
 // ncu sees 35% of the tensor pipe and 38% of the issue slots busy with the cap.
-// At 4 x 16(4) x 4096 x 128 causal, capped, the call takes 1000 us (687 GFLOP)
-// against 1010 us of the plain backward in the same run.
+// At 4 x 16(4) x 4096 x 128 causal (687 GFLOP) the call takes 0.99-1.10 ms with a cap
+// and 0.89-0.99 without; with 16 key heads 1.04-1.20 and 0.94-1.10, where the plain
+// backward takes 0.89-0.97 in the same runs (the low ends one call at a time, the
+// high ends back to back under the power cap).
 #pragma once
 #include <cuda_fp16.h>
 

@@ -10,10 +10,10 @@
 // P (1 - t^2) 2^15 in fp16.
 //
 // Bound like the plain pass (the P and dS chain of 256 threads beside three
-// products a tile).  The whole call against the one with atomics: 1417 us against
-// 1037 at 4 x 16(4) x 4096 x 128 causal capped, 370 against 276 at
-// 2 x 16 x 8192 x 64 with documents of 700 tokens and a bias, 91 against 66 at
-// 2 x 8(1) x 2047 x 64 with a window of 511, cap and bias.
+// products a tile).  The whole call against the one with atomics, calls back to
+// back: 1391-1397 us against 1069-1095 at 4 x 16(4) x 4096 x 128 causal capped, 370
+// against 272 at 2 x 16 x 8192 x 64 with documents of 700 tokens and a bias, 96
+// against 64 at 2 x 8(1) x 2047 x 64 with a window of 512, cap and bias.
 #pragma once
 #include "fa_bwd_dq.cuh"
 #include "fa_mod_bwd.cuh"

@@ -36,9 +36,9 @@
 // What bounds it is the chain of a score tile through one softmax warpgroup
 // (load, tanh, maximum, exponentials, store), of which two run side by side: at
 // 4 x 16(4) x 4096 x 128 causal, ncu sees 42% of the issue slots, 26% of the
-// tensor pipe, 26% of MUFU and 24% of the FMA pipes busy.  That size takes 300 us
-// with neither cap nor bias (275 GFLOP: 916 TFLOP/s), 367 us with the bias,
-// 475 us with the cap.  Measured and not kept: the score row transformed in
+// tensor pipe, 26% of MUFU and 24% of the FMA pipes busy.  That size takes 300-326
+// us with neither cap nor bias (275 GFLOP: 843-916 TFLOP/s), 358-376 us with the
+// bias, 473-481 us with the cap, by box, calls back to back.  Measured and not kept: the score row transformed in
 // rolled 32-column steps through tensor memory (470 us capped, but 727 against
 // 687 us biased at 16384 tokens); the maximum taken of the raw scores and tanh
 // and exponential in one loop (509 against 493 us).
@@ -580,8 +580,9 @@ __global__ void __launch_bounds__(384, 1)
       }
       const float l = f2_sum(lsum[0]) + f2_sum(lsum[1]);
       const float r = f2_sum(rsum[0]) + f2_sum(rsum[1]);
-      // an exact zero: a row that saw nothing (a visible key adds at least
-      // 2^-16 to the sums; NaN scores give NaN sums and stay NaN)
+      // an exact zero: a row that saw nothing (else the key that set the reference
+      // maximum has added 1 since the sums were last rescaled; NaN scores give NaN
+      // sums and stay NaN)
       const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / r;
       const uint64_t inv2 = f2_pack(inv, inv);

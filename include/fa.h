@@ -192,7 +192,14 @@ fa_status fa_decode_fwd(const void* q, const void* k_cache, const void* v_cache,
  * keys beside it, masked ones among them.
  * A query that sees no key gets O = 0, LSE = -inf and no gradient; a key that
  * no query sees gets dK = dV = 0.  K and V must be finite also in rows that
- * are masked (padding): they enter products with weight 0. */
+ * are masked (padding), for the backward pass Q, O and dO too: they enter products
+ * with weight 0.
+ * Precision: sums, softmax statistics and scores are fp32; what enters a matrix
+ * product is 16 bits wide, the forward's weights, P for dV and dS for dQ and dK bf16
+ * (relative error of the gradients 2.4e-3 to 2.9e-3, where their own rounding to bf16 has
+ * 1.7e-3), the weights of the cache decode fp16.  The backward pass recomputes
+ * P = exp(score - LSE), which is off by some 2^-22 of the score's size: scores (with
+ * their bias) beyond a few thousand cost bits of the gradients. */
 
 /* Mask plan: for each query one interval of keys [lo, hi), from any of
  *   doc_ids     int32 [B, N] or NULL: query i sees the keys of the run of equal
