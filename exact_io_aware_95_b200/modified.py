@@ -13,6 +13,7 @@ from functools import lru_cache
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _check, _need, _need_shape, _need_workspace, _on, _same_device, _scale, _stream_ptr, lib
@@ -191,9 +192,7 @@ def mod_bwd(q, k, v, o, lse, do, plan: MaskPlan, softcap: float = 0.0, slopes: O
 
 class _ModAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, plan, softcap, slopes, scale, deterministic, recording):
-        if not (recording and any(ctx.needs_input_grad[:3])):  # no backward pass will follow
-            return mod_fwd(q, k, v, plan, softcap=softcap, slopes=slopes, scale=scale)[0]
+    def forward(ctx, q, k, v, plan, softcap, slopes, scale, deterministic):
         o, lse, o_low = mod_fwd(q, k, v, plan, softcap=softcap, slopes=slopes, scale=scale, low=True)
         ctx.save_for_backward(q, k, v, o, lse, o_low, plan.data, *(() if slopes is None else (slopes,)))
         ctx.sizes, ctx.softcap, ctx.scale, ctx.deterministic = (plan.B, plan.N), softcap, scale, deterministic
@@ -206,7 +205,15 @@ class _ModAttention(torch.autograd.Function):
         g = mod_bwd(q, k, v, o, lse, do.contiguous(), MaskPlan(data, *ctx.sizes), softcap=ctx.softcap,
                     slopes=slopes[0] if slopes else None, scale=ctx.scale, o_low=o_low,
                     deterministic=ctx.deterministic)
-        return (*g, None, None, None, None, None, None)
+        return (*g, None, None, None, None, None)
+
+
+def _differentiated(*ts) -> bool:
+    """Some derivative is asked for: a gradient, or a tangent of forward mode (which
+    the Function lacks and refuses)."""
+    ts = [t for t in ts if isinstance(t, torch.Tensor)]
+    return (torch.is_grad_enabled() and any(t.requires_grad for t in ts)) or \
+        any(forward_ad.unpack_dual(t).tangent is not None for t in ts)
 
 
 def mod_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskPlan, softcap: float = 0.0,
@@ -217,6 +224,6 @@ def mod_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: MaskP
     deterministic=True makes the gradients bitwise reproducible."""
     if isinstance(q, torch.Tensor) and q.dim() == 4:
         _slopes(slopes, q.shape[2])  # inside a Function no tensor asks for a gradient
-    # Always through the Function, also where no gradient is asked for: a derivative
-    # that it lacks (forward mode) is refused, not dropped.
-    return _ModAttention.apply(q, k, v, plan, softcap, slopes, scale, bool(deterministic), torch.is_grad_enabled())
+    if not _differentiated(q, k, v, slopes):
+        return mod_fwd(q, k, v, plan, softcap=softcap, slopes=slopes, scale=scale)[0]
+    return _ModAttention.apply(q, k, v, plan, softcap, slopes, scale, bool(deterministic))
