@@ -38,10 +38,10 @@
 // 4 x 16(4) x 4096 x 128 causal, ncu sees 42% of the issue slots, 26% of the
 // tensor pipe, 26% of MUFU and 24% of the FMA pipes busy.  That size takes 300-326
 // us with neither cap nor bias (275 GFLOP: 843-916 TFLOP/s), 358-376 us with the
-// bias, 473-481 us with the cap, by box, calls back to back.  Measured and not kept: the score row transformed in
-// rolled 32-column steps through tensor memory (470 us capped, but 727 against
-// 687 us biased at 16384 tokens); the maximum taken of the raw scores and tanh
-// and exponential in one loop (509 against 493 us).
+// bias, 473-481 us with the cap, by card, calls back to back.  Measured and not
+// kept: the score row transformed in rolled 32-column steps through tensor memory
+// (470 us capped, but 727 against 687 us biased at 16384 tokens); the maximum taken
+// of the raw scores and tanh and exponential in one loop (509 against 493 us).
 #pragma once
 #include "fa_fwd.cuh"
 #include "fa_plan.cuh"
